@@ -315,6 +315,92 @@ nvfp4_status nvfp4_mx_gemm_residue(const uint8_t* a_codes, const uint8_t* a_scal
                                    int64_t M, int64_t N, int64_t K, void* y, nvfp4_dtype out_dt, int64_t ldy,
                                    int* dev_status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * 8-bit integer linear and layer norm.  The pages have no counterpart: these
+ * serve the layers of a model that do not survive 4 bits (W8A8 with a scale
+ * for each token and each output channel) and the models whose norm is a layer
+ * norm; their inputs, layouts and errors follow the entry points above.
+ * ------------------------------------------------------------------------ */
+
+/* Longest row of the entry points below: K * 128 * 128 < 2^31, so the product's
+ * int32 sums cannot overflow (codes of -128 included). */
+#define NVFP4_I8_MAX_K 131056
+
+/* Rows of X (M x K, dtype dt, row stride ldx) in 8 bits, one scale per row
+ * (a token of the activations, an output channel of a weight):
+ *   amax = max|x_row|;  scale = fl32(amax / 127)
+ *   code = rint(fl32(x * fl32(127 / amax)))            (ties to even, |code| <= 127)
+ * amax < 2^-110 gives scale 0 and codes 0.  A row with a NaN or an infinity
+ * gets scale NaN and codes 0 (its products are NaN) and sets
+ * NVFP4_ERR_NONFINITE in *dev_status.
+ * x: device, 16-byte aligned, ldx * sizeof(dt) a multiple of 16; K % 16 == 0,
+ *   K <= NVFP4_I8_MAX_K (else NVFP4_ERR_UNSUPPORTED).
+ * codes: device, M rows of K bytes with row stride ldc >= K, 16-byte aligned,
+ *   ldc % 16 == 0; bytes between rows are left as they are.
+ * scales: device, M floats.  Outputs must not overlap x. */
+nvfp4_status nvfp4_i8_quantize(const void* x, nvfp4_dtype dt, int64_t M, int64_t K, int64_t ldx, int8_t* codes,
+                               int64_t ldc, float* scales, int* dev_status, void* stream);
+
+/* Layer norm over the rows of X (M x K, dtype dt):
+ *   mean = fl32(sum(x) / K);  d = fl32(x - mean)
+ *   rstd = fl32(1 / sqrt(sum(d^2) / K + eps))          (both sums in binary64)
+ *   y    = fl32(fl32(fl32(d * rstd) * gamma) + beta)   (then rounded to dt)
+ * gamma, beta: device, K elements of dtype pdt, 16-byte aligned, each may be
+ *   NULL (1 and 0).  eps >= 0.
+ * y: device, dtype dt, row stride ldy, aligned as x.
+ * mean, rstd: device, M floats each, what the backward pass reads, or NULL.
+ * y may be x itself (same pointer and stride) when K <= 8192.
+ * A row with a NaN or an infinity gives NaN and sets NVFP4_ERR_NONFINITE in
+ * *dev_status; so does eps = 0 with a constant row.  x and K as
+ * nvfp4_i8_quantize. */
+nvfp4_status nvfp4_layernorm(const void* x, nvfp4_dtype dt, int64_t M, int64_t K, int64_t ldx, const void* gamma,
+                             const void* beta, nvfp4_dtype pdt, float eps, void* y, int64_t ldy, float* mean,
+                             float* rstd, int* dev_status, void* stream);
+
+/* nvfp4_layernorm, its fp32 result (before the rounding to dt) quantized as by
+ * nvfp4_i8_quantize, in one pass: the input of nvfp4_i8_gemm.  Arguments as the
+ * two calls. */
+nvfp4_status nvfp4_layernorm_i8_quantize(const void* x, nvfp4_dtype dt, int64_t M, int64_t K, int64_t ldx,
+                                         const void* gamma, const void* beta, nvfp4_dtype pdt, float eps,
+                                         int8_t* codes, int64_t ldc, float* scales, int* dev_status, void* stream);
+
+/* Bytes of workspace nvfp4_layernorm_backward needs for the parameters'
+ * gradients (0 for an empty input).  It needs no initialisation and holds
+ * nothing between calls; calls sharing it must be ordered (same stream). */
+size_t nvfp4_layernorm_workspace_size(int64_t M, int64_t K);
+
+/* Gradients of nvfp4_layernorm: with xh = (x - mean) * rstd, g = dy * gamma,
+ *   dx     = rstd * (g - sum(g) / K - xh * sum(g * xh) / K)   (sums over a row)
+ *   dgamma = sum(dy * xh),  dbeta = sum(dy)                   (sums over the rows)
+ * in fp32; dx is rounded to dt, dgamma and dbeta stay fp32.  The sums are formed
+ * in a fixed order: the same call gives the same bits.
+ * dy, x: device, dtype dt, aligned as nvfp4_layernorm's x; gamma as there.
+ * mean, rstd: the forward call's statistics.
+ * dx, dgamma (K floats), dbeta (K floats): device, each may be NULL (at least
+ *   one is not); dx must not overlap dy or x.
+ * workspace: >= nvfp4_layernorm_workspace_size(M, K) bytes, 16-byte aligned
+ *   (used when dgamma or dbeta is wanted). */
+nvfp4_status nvfp4_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, nvfp4_dtype dt,
+                                      int64_t M, int64_t K, const void* gamma, nvfp4_dtype pdt, const float* mean,
+                                      const float* rstd, void* dx, int64_t lddx, float* dgamma, float* dbeta,
+                                      void* workspace, size_t ws_bytes, void* stream);
+
+/* 8-bit integer linear with a scale for each token and each output channel:
+ *   acc  = sum_k a[m, k] * w[n, k]                            (int32, exact)
+ *   y    = fl32(fl32(fl32(acc) * a_scales[m]) * w_scales[n])  (+ bias[n], rounded)
+ * then rounded to out_dt.  a_codes (M x K) and w_codes (N x K): device, int8,
+ * row strides lda, ldw (multiples of 16), 16-byte aligned; K % 16 == 0,
+ * K <= NVFP4_I8_MAX_K (else NVFP4_ERR_UNSUPPORTED); any M >= 1 and N >= 1 up to
+ * 2^31 - 4097.
+ * a_scales: M floats; w_scales, bias: N floats; bias may be NULL.
+ * y: device, aligned to sizeof(out_dt), row stride ldy >= N; must not overlap
+ * the inputs.  The kernels may start before the preceding kernel on `stream`
+ * has finished (programmatic dependent launch); they read nothing that kernel
+ * produces until it has completed. */
+nvfp4_status nvfp4_i8_gemm(const int8_t* a_codes, int64_t lda, const float* a_scales, const int8_t* w_codes,
+                           int64_t ldw, const float* w_scales, const float* bias, int64_t M, int64_t N, int64_t K,
+                           void* y, nvfp4_dtype out_dt, int64_t ldy, int* dev_status, void* stream);
+
 /* Test support for the device-side bounded waits (failure detection around
  * the method; the pages have no counterpart).  Every mbarrier wait of the
  * tensor-core kernels (nvfp4_gemm, nvfp4_gemm_residue, the fused decode

@@ -29,8 +29,11 @@ EXPORTED_SYMBOLS = ("nvfp4_scales_bytes", "nvfp4_workspace_size", "nvfp4_quantiz
                     "nvfp4_quantize_gemm_plan", "nvfp4_quantize_gemm_host",
                     "nvfp4_rmsnorm_reorder_quantize_noalloc", "nvfp4_mx_quantize",
                     "nvfp4_mx_scales_bytes", "nvfp4_mx_gemm", "nvfp4_mx_gemm_residue", "nvfp4_quantize_weight",
+                    "nvfp4_i8_quantize", "nvfp4_i8_gemm", "nvfp4_layernorm", "nvfp4_layernorm_i8_quantize",
+                    "nvfp4_layernorm_backward", "nvfp4_layernorm_workspace_size",
                     "nvfp4_test_wait_fault", "nvfp4_status_string", "nvfp4_version")
 NVFP4_NOALLOC_MAX_ROWS = 65536
+NVFP4_I8_MAX_K = 131056
 
 
 class NVFP4Error(RuntimeError):
@@ -87,6 +90,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
             getattr(lib, fn).restype = ctypes.c_int
         lib.nvfp4_quantize_weight.argtypes = [P, ctypes.c_int, I64, I64, I64, P, P, I64, P, T, P, SZ, P, P]
         lib.nvfp4_quantize_weight.restype = ctypes.c_int
+        I = ctypes.c_int
+        lib.nvfp4_i8_quantize.argtypes = [P, I, I64, I64, I64, P, I64, P, P, P]
+        lib.nvfp4_layernorm.argtypes = [P, I, I64, I64, I64, P, P, I, F, P, I64, P, P, P, P]
+        lib.nvfp4_layernorm_i8_quantize.argtypes = [P, I, I64, I64, I64, P, P, I, F, P, I64, P, P, P]
+        lib.nvfp4_layernorm_backward.argtypes = [P, I64, P, I64, I, I64, I64, P, I, P, P, P, I64, P, P, P, SZ, P]
+        lib.nvfp4_i8_gemm.argtypes = [P, I64, P, P, I64, P, P, I64, I64, I64, P, I, I64, P, P]
+        lib.nvfp4_layernorm_workspace_size.argtypes = [I64, I64]
+        lib.nvfp4_layernorm_workspace_size.restype = SZ
+        for fn in ("nvfp4_i8_quantize", "nvfp4_layernorm", "nvfp4_layernorm_i8_quantize",
+                   "nvfp4_layernorm_backward", "nvfp4_i8_gemm"):
+            getattr(lib, fn).restype = I
         lib.nvfp4_test_wait_fault.argtypes = [ctypes.c_uint64, ctypes.c_int]
         lib.nvfp4_test_wait_fault.restype = None
         lib.nvfp4_status_string.argtypes = [ctypes.c_int]
@@ -424,3 +438,147 @@ def nvfp4_quantize_gemm_plan(M: int, N: int, K: int, x_dtype=torch.bfloat16, res
     lib = load_library()
     code = lambda d: NVFP4_BF16 if d == torch.bfloat16 else NVFP4_F32
     return lib.nvfp4_quantize_gemm_plan(M, N, K, code(x_dtype), 1 if residue else 0, code(out_dtype))
+
+
+# ------------------------------------------------ 8-bit integer linear, layer norm
+
+def _device(where: str, *tensors: Optional[torch.Tensor]) -> int:
+    """Index of the one CUDA device of the tensors given (None among them is skipped)."""
+    dev = tensors[0].get_device()           # -1: not on a GPU
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: tensors are on different devices")
+    if dev < 0:
+        raise ValueError(f"{where}: tensors must be on a CUDA device")
+    return dev
+
+
+def _rows(t: torch.Tensor, M: int, K: int, dtype, where: str, name: str) -> int:
+    """Row stride of a 2-D row-major tensor of this shape and dtype."""
+    if t.dtype is not dtype or t.shape != (M, K):
+        raise ValueError(f"{where}: {name} must be a row-major {M} x {K} tensor of {dtype}")
+    ld, step = t.stride()
+    if step != 1 and K > 1:
+        raise ValueError(f"{where}: {name} must be row-major")
+    return ld if M > 1 else (K + 15) // 16 * 16      # one row: its stride is never used
+
+
+def _vector(t: Optional[torch.Tensor], n: int, dtype, where: str, name: str) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be a contiguous tensor of {n} {dtype} elements")
+    return t.data_ptr()
+
+
+def _params(gamma, beta, K: int, where: str):
+    """(gamma, beta, dtype code) of a layer norm's parameters; both have one dtype."""
+    some = gamma if gamma is not None else beta
+    if some is None:
+        return None, None, NVFP4_F32
+    dtype = some.dtype
+    return _vector(gamma, K, dtype, where, "gamma"), _vector(beta, K, dtype, where, "beta"), _dtype_code(some)
+
+
+def _call(dev: int, stream, where: str, fn, *args) -> None:
+    """fn(*args, stream) with the tensors' device current, on its current stream unless one is given."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(stream)), where)
+        return
+    status = fn(*args, _stream(stream))
+    if status:
+        raise NVFP4Error(status, where)
+
+
+def nvfp4_i8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                      dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rows of x (M x K) in 8 bits: codes int8 M x K, scales float32 [M] (scale = amax / 127 of the row)."""
+    where = "nvfp4_i8_quantize"
+    M, K = x.shape
+    ldx, ldc = _rows(x, M, K, x.dtype, where, "x"), _rows(codes, M, K, torch.int8, where, "codes")
+    sp = _vector(scales, M, torch.float32, where, "scales")
+    dev = _device(where, x, codes, scales, dev_status)
+    _call(dev, stream, where, load_library().nvfp4_i8_quantize, x.data_ptr(), _dtype_code(x), M, K, ldx,
+          codes.data_ptr(), ldc, sp, _ptr(dev_status))
+
+
+def nvfp4_layernorm(x: torch.Tensor, y: torch.Tensor, gamma: Optional[torch.Tensor] = None,
+                    beta: Optional[torch.Tensor] = None, eps: float = 1e-5, mean: Optional[torch.Tensor] = None,
+                    rstd: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """y = layer norm of the rows of x; mean, rstd (float32 [M]): the statistics the backward pass reads."""
+    where = "nvfp4_layernorm"
+    M, K = x.shape
+    ldx, ldy = _rows(x, M, K, x.dtype, where, "x"), _rows(y, M, K, x.dtype, where, "y")
+    gp, bp, pdt = _params(gamma, beta, K, where)
+    mp, rp = _vector(mean, M, torch.float32, where, "mean"), _vector(rstd, M, torch.float32, where, "rstd")
+    dev = _device(where, x, y, gamma, beta, mean, rstd, dev_status)
+    _call(dev, stream, where, load_library().nvfp4_layernorm, x.data_ptr(), _dtype_code(x), M, K, ldx, gp, bp, pdt,
+          eps, y.data_ptr(), ldy, mp, rp, _ptr(dev_status))
+
+
+def nvfp4_layernorm_i8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                                gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None,
+                                eps: float = 1e-5, dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Layer norm of the rows of x, in 8 bits (nvfp4_i8_quantize of its fp32 result)."""
+    where = "nvfp4_layernorm_i8_quantize"
+    M, K = x.shape
+    ldx, ldc = _rows(x, M, K, x.dtype, where, "x"), _rows(codes, M, K, torch.int8, where, "codes")
+    sp = _vector(scales, M, torch.float32, where, "scales")
+    gp, bp, pdt = _params(gamma, beta, K, where)
+    dev = _device(where, x, codes, scales, gamma, beta, dev_status)
+    _call(dev, stream, where, load_library().nvfp4_layernorm_i8_quantize, x.data_ptr(), _dtype_code(x), M, K, ldx,
+          gp, bp, pdt, eps, codes.data_ptr(), ldc, sp, _ptr(dev_status))
+
+
+def nvfp4_layernorm_workspace_size(M: int, K: int) -> int:
+    return int(load_library().nvfp4_layernorm_workspace_size(M, K))
+
+
+class LayerNormWorkspace:
+    """Workspace of nvfp4_layernorm_backward (nvfp4_layernorm_workspace_size): no initialisation, nothing kept."""
+
+    def __init__(self, M: int, K: int, device="cuda"):
+        self.nbytes = nvfp4_layernorm_workspace_size(M, K)
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+
+    def ptr(self) -> int:
+        return self.buf.data_ptr()
+
+
+def nvfp4_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                             dx: Optional[torch.Tensor] = None, gamma: Optional[torch.Tensor] = None,
+                             dgamma: Optional[torch.Tensor] = None, dbeta: Optional[torch.Tensor] = None,
+                             workspace: Optional[LayerNormWorkspace] = None, stream=None) -> None:
+    """Gradients of nvfp4_layernorm: dx (x's dtype), dgamma and dbeta (float32 [K]); those that are None are
+    not computed.  mean, rstd: the forward call's."""
+    where = "nvfp4_layernorm_backward"
+    M, K = x.shape
+    ldx, lddy = _rows(x, M, K, x.dtype, where, "x"), _rows(dy, M, K, x.dtype, where, "dy")
+    lddx = _rows(dx, M, K, x.dtype, where, "dx") if dx is not None else K
+    gp, _, pdt = _params(gamma, None, K, where)
+    mp, rp = _vector(mean, M, torch.float32, where, "mean"), _vector(rstd, M, torch.float32, where, "rstd")
+    dgp = _vector(dgamma, K, torch.float32, where, "dgamma")
+    dbp = _vector(dbeta, K, torch.float32, where, "dbeta")
+    ws_ptr, ws_n = (workspace.ptr(), workspace.nbytes) if workspace is not None else (None, 0)
+    dev = _device(where, x, dy, mean, rstd, dx, gamma, dgamma, dbeta, workspace.buf if workspace is not None else None)
+    _call(dev, stream, where, load_library().nvfp4_layernorm_backward, dy.data_ptr(), lddy, x.data_ptr(), ldx,
+          _dtype_code(x), M, K, gp, pdt, mp, rp, _ptr(dx), lddx, dgp, dbp, ws_ptr, ws_n)
+
+
+def nvfp4_i8_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                  y: torch.Tensor, bias: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """8-bit linear y = (a w^T) * a_scales[:, None] * w_scales (+ bias): a_codes int8 M x K, w_codes int8 N x K,
+    scales and bias float32, y M x N float32 or bfloat16."""
+    where = "nvfp4_i8_gemm"
+    M, K = a_codes.shape
+    N = w_codes.shape[0]
+    lda, ldw = _rows(a_codes, M, K, torch.int8, where, "a_codes"), _rows(w_codes, N, K, torch.int8, where, "w_codes")
+    ldy = _rows(y, M, N, y.dtype, where, "y")
+    ap, wp = _vector(a_scales, M, torch.float32, where, "a_scales"), _vector(w_scales, N, torch.float32, where, "w_scales")
+    bp = _vector(bias, N, torch.float32, where, "bias")
+    dev = _device(where, a_codes, a_scales, w_codes, w_scales, y, bias, dev_status)
+    _call(dev, stream, where, load_library().nvfp4_i8_gemm, a_codes.data_ptr(), lda, ap, w_codes.data_ptr(), ldw, wp,
+          bp, M, N, K, y.data_ptr(), _out_dtype(y), ldy, _ptr(dev_status))

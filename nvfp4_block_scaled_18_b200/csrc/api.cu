@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "common.cuh"
@@ -143,6 +144,25 @@ nvfp4_status run_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const 
   const cudaError_t e = launch_gemm_mx(g, num_sms_current_device(), static_cast<cudaStream_t>(stream));
   if (e == cudaErrorNotSupported) return NVFP4_ERR_UNSUPPORTED;
   return cuda_status(e);
+}
+
+// -- 8-bit integer linear, layer norm
+constexpr int64_t kI8MaxK = NVFP4_I8_MAX_K, kI8MaxRows = INT32_MAX - 4096;
+
+nvfp4_status check_rows(const void* p, nvfp4_dtype dt, int64_t K, int64_t ld) {
+  if (p == nullptr || ld < K) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(p) || ((size_t)ld * dt_size(dt)) % 16 != 0) return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+nvfp4_status check_i8_out(const int8_t* codes, int64_t K, int64_t ldc, const float* scales) {
+  if (codes == nullptr || scales == nullptr || ldc < K) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(codes) || ldc % 16 != 0 || (reinterpret_cast<uintptr_t>(scales) & 3u)) return NVFP4_ERR_ALIGNMENT;
+  return NVFP4_OK;
+}
+nvfp4_status check_norm(const void* gamma, const void* beta, nvfp4_dtype pdt, float eps) {
+  if (!dt_ok(pdt) || !(eps >= 0.0f)) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(gamma) || !aligned16(beta)) return NVFP4_ERR_ALIGNMENT;   // null counts as aligned
+  return NVFP4_OK;
 }
 
 }  // namespace
@@ -398,6 +418,95 @@ nvfp4_status nvfp4_mx_gemm_residue(const uint8_t* a_codes, const uint8_t* a_scal
   if (r_codes == nullptr || r_scales == nullptr) return NVFP4_ERR_INVALID_ARG;
   return run_mx_gemm(a_codes, a_scales, r_codes, r_scales, w_codes, w_scales, M, N, K, y, out_dt, ldy, dev_status,
                      stream);
+}
+
+// ------------------------------------------ 8-bit integer linear, layer norm
+
+nvfp4_status nvfp4_i8_quantize(const void* x, nvfp4_dtype dt, int64_t M, int64_t K, int64_t ldx, int8_t* codes,
+                               int64_t ldc, float* scales, int* dev_status, void* stream) {
+  NVFP4_TRY(check_input(x, dt, M, K, ldx));
+  NVFP4_TRY(check_i8_out(codes, K, ldc, scales));
+  if (K > kI8MaxK) return NVFP4_ERR_UNSUPPORTED;
+  return cuda_status(launch_i8_quant(x, dt, M, K, ldx, codes, ldc, scales, dev_status, num_sms_current_device(),
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_layernorm(const void* x, nvfp4_dtype dt, int64_t M, int64_t K, int64_t ldx, const void* gamma,
+                             const void* beta, nvfp4_dtype pdt, float eps, void* y, int64_t ldy, float* mean,
+                             float* rstd, int* dev_status, void* stream) {
+  NVFP4_TRY(check_input(x, dt, M, K, ldx));
+  NVFP4_TRY(check_rows(y, dt, K, ldy));
+  NVFP4_TRY(check_norm(gamma, beta, pdt, eps));
+  if ((reinterpret_cast<uintptr_t>(mean) & 3u) || (reinterpret_cast<uintptr_t>(rstd) & 3u)) return NVFP4_ERR_ALIGNMENT;
+  if (K > kI8MaxK) return NVFP4_ERR_UNSUPPORTED;
+  LayerNormArgs n{};
+  n.x = x; n.ldx = ldx; n.dt = dt; n.gamma = gamma; n.beta = beta; n.pdt = pdt; n.eps = eps;
+  n.y = y; n.ldy = ldy; n.mean = mean; n.rstd = rstd; n.M = M; n.K = K; n.st = dev_status;
+  return cuda_status(launch_layernorm(n, num_sms_current_device(), static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_layernorm_i8_quantize(const void* x, nvfp4_dtype dt, int64_t M, int64_t K, int64_t ldx,
+                                         const void* gamma, const void* beta, nvfp4_dtype pdt, float eps,
+                                         int8_t* codes, int64_t ldc, float* scales, int* dev_status, void* stream) {
+  NVFP4_TRY(check_input(x, dt, M, K, ldx));
+  NVFP4_TRY(check_i8_out(codes, K, ldc, scales));
+  NVFP4_TRY(check_norm(gamma, beta, pdt, eps));
+  if (K > kI8MaxK) return NVFP4_ERR_UNSUPPORTED;
+  LayerNormArgs n{};
+  n.x = x; n.ldx = ldx; n.dt = dt; n.gamma = gamma; n.beta = beta; n.pdt = pdt; n.eps = eps;
+  n.codes = codes; n.ldc = ldc; n.scales = scales; n.M = M; n.K = K; n.st = dev_status;
+  return cuda_status(launch_layernorm(n, num_sms_current_device(), static_cast<cudaStream_t>(stream)));
+}
+
+size_t nvfp4_layernorm_workspace_size(int64_t M, int64_t K) {
+  if (M <= 0 || K <= 0) return 0;
+  return (size_t)layernorm_parts(M) * 2 * (size_t)K * sizeof(float);
+}
+
+nvfp4_status nvfp4_layernorm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, nvfp4_dtype dt,
+                                      int64_t M, int64_t K, const void* gamma, nvfp4_dtype pdt, const float* mean,
+                                      const float* rstd, void* dx, int64_t lddx, float* dgamma, float* dbeta,
+                                      void* workspace, size_t ws_bytes, void* stream) {
+  NVFP4_TRY(check_input(x, dt, M, K, ldx));
+  NVFP4_TRY(check_input(dy, dt, M, K, lddy));
+  NVFP4_TRY(check_norm(gamma, nullptr, pdt, 0.0f));
+  if (mean == nullptr || rstd == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (dx == nullptr && dgamma == nullptr && dbeta == nullptr) return NVFP4_ERR_INVALID_ARG;
+  if (dx != nullptr) NVFP4_TRY(check_rows(dx, dt, K, lddx));
+  for (const float* p : {mean, rstd, (const float*)dgamma, (const float*)dbeta})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return NVFP4_ERR_ALIGNMENT;
+  if (K > kI8MaxK) return NVFP4_ERR_UNSUPPORTED;
+  if (dgamma != nullptr || dbeta != nullptr) {
+    if (workspace == nullptr || ws_bytes < nvfp4_layernorm_workspace_size(M, K)) return NVFP4_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return NVFP4_ERR_ALIGNMENT;
+  }
+  LayerNormBwdArgs n{};
+  n.dy = dy; n.lddy = lddy; n.x = x; n.ldx = ldx; n.dt = dt; n.gamma = gamma; n.pdt = pdt;
+  n.mean = mean; n.rstd = rstd; n.dx = dx; n.lddx = lddx; n.dgamma = dgamma; n.dbeta = dbeta;
+  n.part = static_cast<float*>(workspace); n.M = M; n.K = K;
+  return cuda_status(launch_layernorm_backward(n, num_sms_current_device(), static_cast<cudaStream_t>(stream)));
+}
+
+nvfp4_status nvfp4_i8_gemm(const int8_t* a_codes, int64_t lda, const float* a_scales, const int8_t* w_codes,
+                           int64_t ldw, const float* w_scales, const float* bias, int64_t M, int64_t N, int64_t K,
+                           void* y, nvfp4_dtype out_dt, int64_t ldy, int* dev_status, void* stream) {
+  if (a_codes == nullptr || a_scales == nullptr || w_codes == nullptr || w_scales == nullptr || y == nullptr ||
+      !dt_ok(out_dt))
+    return NVFP4_ERR_INVALID_ARG;
+  if (M <= 0 || N <= 0 || K <= 0 || K % 16 != 0 || lda < K || ldw < K || ldy < N) return NVFP4_ERR_INVALID_ARG;
+  if (!aligned16(a_codes) || !aligned16(w_codes) || lda % 16 != 0 || ldw % 16 != 0) return NVFP4_ERR_ALIGNMENT;
+  if ((reinterpret_cast<uintptr_t>(y) % dt_size(out_dt)) != 0) return NVFP4_ERR_ALIGNMENT;
+  for (const float* p : {a_scales, w_scales, bias})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return NVFP4_ERR_ALIGNMENT;
+  // int32 sums; 32-bit rows and columns with room for a partial tile; 40-bit row pitches of a tensor map
+  if (K > kI8MaxK || M > kI8MaxRows || N > kI8MaxRows || lda >= (1ll << 40) || ldw >= (1ll << 40))
+    return NVFP4_ERR_UNSUPPORTED;
+  I8GemmArgs g{};
+  g.a = a_codes; g.lda = lda; g.a_scales = a_scales; g.w = w_codes; g.ldw = ldw; g.w_scales = w_scales;
+  g.bias = bias; g.y = y; g.ldy = ldy; g.y_bf16 = out_dt == NVFP4_BF16; g.M = M; g.N = N; g.K = K; g.st = dev_status;
+  const cudaError_t e = launch_i8_gemm(g, num_sms_current_device(), static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return NVFP4_ERR_UNSUPPORTED;
+  return cuda_status(e);
 }
 
 const char* nvfp4_status_string(nvfp4_status st) {

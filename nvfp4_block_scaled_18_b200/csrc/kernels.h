@@ -126,4 +126,43 @@ cudaError_t launch_mx_quant(const void* x, nvfp4_dtype dt, int64_t M, int64_t K,
                             cudaStream_t stream);
 cudaError_t launch_gemv_tc(const GemmArgs& g, int num_sms, cudaStream_t stream);
 
+// Layer norm and the 8-bit integer linear.
+// Rows of x (M x K) in 8 bits: one scale per row.
+cudaError_t launch_i8_quant(const void* x, nvfp4_dtype dt, int64_t M, int64_t K, int64_t ldx, int8_t* codes,
+                            int64_t ldc, float* scales, int* st, int num_sms, cudaStream_t stream);
+struct LayerNormArgs {
+  const void* x; int64_t ldx; nvfp4_dtype dt;
+  const void* gamma; const void* beta; nvfp4_dtype pdt;   // either may be null
+  float eps;
+  void* y; int64_t ldy; float* mean; float* rstd;         // codes == null: y in dt, statistics if asked for
+  int8_t* codes; int64_t ldc; float* scales;              // else y in 8 bits
+  int64_t M, K;
+  int* st;
+};
+cudaError_t launch_layernorm(const LayerNormArgs& n, int num_sms, cudaStream_t stream);
+// Rows of partial parameter gradients in the backward pass's workspace.
+constexpr int kLnMaxParts = 296;
+int layernorm_parts(int64_t M);
+struct LayerNormBwdArgs {
+  const void* dy; int64_t lddy; const void* x; int64_t ldx; nvfp4_dtype dt;
+  const void* gamma; nvfp4_dtype pdt;                     // may be null
+  const float* mean; const float* rstd;
+  void* dx; int64_t lddx;                                 // may be null
+  float* dgamma; float* dbeta;                            // either may be null
+  float* part;                                            // layernorm_parts(M) x 2 x K
+  int64_t M, K;
+};
+cudaError_t launch_layernorm_backward(const LayerNormBwdArgs& n, int num_sms, cudaStream_t stream);
+
+// 8-bit linear: y = (sum_k a w) * a_scales[m] * w_scales[n] (+ bias[n]).
+struct I8GemmArgs {
+  const int8_t* a; int64_t lda; const float* a_scales;    // M x K
+  const int8_t* w; int64_t ldw; const float* w_scales;    // N x K
+  const float* bias;                                      // may be null
+  void* y; int64_t ldy; bool y_bf16;
+  int64_t M, N, K;
+  int* st;
+};
+cudaError_t launch_i8_gemm(const I8GemmArgs& g, int num_sms, cudaStream_t stream);
+
 }  // namespace nvfp4
