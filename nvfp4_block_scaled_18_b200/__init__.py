@@ -495,11 +495,12 @@ def nvfp4_i8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
                       dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Rows of x (M x K) in 8 bits: codes int8 M x K, scales float32 [M] (scale = amax / 127 of the row)."""
     where = "nvfp4_i8_quantize"
+    dt = _dtype_code(x)
     M, K = x.shape
     ldx, ldc = _rows(x, M, K, x.dtype, where, "x"), _rows(codes, M, K, torch.int8, where, "codes")
     sp = _vector(scales, M, torch.float32, where, "scales")
     dev = _device(where, x, codes, scales, dev_status)
-    _call(dev, stream, where, load_library().nvfp4_i8_quantize, x.data_ptr(), _dtype_code(x), M, K, ldx,
+    _call(dev, stream, where, load_library().nvfp4_i8_quantize, x.data_ptr(), dt, M, K, ldx,
           codes.data_ptr(), ldc, sp, _ptr(dev_status))
 
 
@@ -509,12 +510,13 @@ def nvfp4_layernorm(x: torch.Tensor, y: torch.Tensor, gamma: Optional[torch.Tens
                     stream=None) -> None:
     """y = layer norm of the rows of x; mean, rstd (float32 [M]): the statistics the backward pass reads."""
     where = "nvfp4_layernorm"
+    dt = _dtype_code(x)
     M, K = x.shape
     ldx, ldy = _rows(x, M, K, x.dtype, where, "x"), _rows(y, M, K, x.dtype, where, "y")
     gp, bp, pdt = _params(gamma, beta, K, where)
     mp, rp = _vector(mean, M, torch.float32, where, "mean"), _vector(rstd, M, torch.float32, where, "rstd")
     dev = _device(where, x, y, gamma, beta, mean, rstd, dev_status)
-    _call(dev, stream, where, load_library().nvfp4_layernorm, x.data_ptr(), _dtype_code(x), M, K, ldx, gp, bp, pdt,
+    _call(dev, stream, where, load_library().nvfp4_layernorm, x.data_ptr(), dt, M, K, ldx, gp, bp, pdt,
           eps, y.data_ptr(), ldy, mp, rp, _ptr(dev_status))
 
 
@@ -523,12 +525,13 @@ def nvfp4_layernorm_i8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: to
                                 eps: float = 1e-5, dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Layer norm of the rows of x, in 8 bits (nvfp4_i8_quantize of its fp32 result)."""
     where = "nvfp4_layernorm_i8_quantize"
+    dt = _dtype_code(x)
     M, K = x.shape
     ldx, ldc = _rows(x, M, K, x.dtype, where, "x"), _rows(codes, M, K, torch.int8, where, "codes")
     sp = _vector(scales, M, torch.float32, where, "scales")
     gp, bp, pdt = _params(gamma, beta, K, where)
     dev = _device(where, x, codes, scales, gamma, beta, dev_status)
-    _call(dev, stream, where, load_library().nvfp4_layernorm_i8_quantize, x.data_ptr(), _dtype_code(x), M, K, ldx,
+    _call(dev, stream, where, load_library().nvfp4_layernorm_i8_quantize, x.data_ptr(), dt, M, K, ldx,
           gp, bp, pdt, eps, codes.data_ptr(), ldc, sp, _ptr(dev_status))
 
 
@@ -554,6 +557,7 @@ def nvfp4_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tens
     """Gradients of nvfp4_layernorm: dx (x's dtype), dgamma and dbeta (float32 [K]); those that are None are
     not computed.  mean, rstd: the forward call's."""
     where = "nvfp4_layernorm_backward"
+    dt = _dtype_code(x)
     M, K = x.shape
     ldx, lddy = _rows(x, M, K, x.dtype, where, "x"), _rows(dy, M, K, x.dtype, where, "dy")
     lddx = _rows(dx, M, K, x.dtype, where, "dx") if dx is not None else K
@@ -564,7 +568,7 @@ def nvfp4_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tens
     ws_ptr, ws_n = (workspace.ptr(), workspace.nbytes) if workspace is not None else (None, 0)
     dev = _device(where, x, dy, mean, rstd, dx, gamma, dgamma, dbeta, workspace.buf if workspace is not None else None)
     _call(dev, stream, where, load_library().nvfp4_layernorm_backward, dy.data_ptr(), lddy, x.data_ptr(), ldx,
-          _dtype_code(x), M, K, gp, pdt, mp, rp, _ptr(dx), lddx, dgp, dbp, ws_ptr, ws_n)
+          dt, M, K, gp, pdt, mp, rp, _ptr(dx), lddx, dgp, dbp, ws_ptr, ws_n)
 
 
 def nvfp4_i8_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
@@ -573,6 +577,7 @@ def nvfp4_i8_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.
     """8-bit linear y = (a w^T) * a_scales[:, None] * w_scales (+ bias): a_codes int8 M x K, w_codes int8 N x K,
     scales and bias float32, y M x N float32 or bfloat16."""
     where = "nvfp4_i8_gemm"
+    out_dt = _out_dtype(y)
     M, K = a_codes.shape
     N = w_codes.shape[0]
     lda, ldw = _rows(a_codes, M, K, torch.int8, where, "a_codes"), _rows(w_codes, N, K, torch.int8, where, "w_codes")
@@ -581,4 +586,4 @@ def nvfp4_i8_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.
     bp = _vector(bias, N, torch.float32, where, "bias")
     dev = _device(where, a_codes, a_scales, w_codes, w_scales, y, bias, dev_status)
     _call(dev, stream, where, load_library().nvfp4_i8_gemm, a_codes.data_ptr(), lda, ap, w_codes.data_ptr(), ldw, wp,
-          bp, M, N, K, y.data_ptr(), _out_dtype(y), ldy, _ptr(dev_status))
+          bp, M, N, K, y.data_ptr(), out_dt, ldy, _ptr(dev_status))
