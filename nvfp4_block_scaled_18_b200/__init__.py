@@ -480,13 +480,19 @@ def _params(gamma, beta, K: int, where: str):
     return _vector(gamma, K, dtype, where, "gamma"), _vector(beta, K, dtype, where, "beta"), _dtype_code(some)
 
 
+# the current stream as an address, without building a stream object (3 us of a call that takes 8)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _call(dev: int, stream, where: str, fn, *args) -> None:
     """fn(*args, stream) with the tensors' device current, on its current stream unless one is given."""
-    if dev != torch.cuda.current_device():
+    raw = _raw_stream(dev) if stream is None else _stream(stream)
+    if dev == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(stream)), where)
-        return
-    status = fn(*args, _stream(stream))
+            status = fn(*args, raw)
     if status:
         raise NVFP4Error(status, where)
 

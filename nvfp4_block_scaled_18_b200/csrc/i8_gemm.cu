@@ -330,7 +330,8 @@ cudaError_t launch_tiles(const I8GemmArgs& g, int bn, int num_sms, cudaStream_t 
   const WaitTest wt = wait_test();
   p.wait_ns = wt.limit_ns; p.hold = wt.hold;
   auto kern = g.y_bf16 ? k_i8_gemm<CG, true> : k_i8_gemm<CG, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  static SmemOnce once[2];
+  cudaError_t e = once[g.y_bf16 ? 1 : 0].set(kern, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(CG * std::max(1, std::min(p.num_tiles, num_sms / CG))));

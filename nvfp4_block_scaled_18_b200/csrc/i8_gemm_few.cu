@@ -284,7 +284,8 @@ cudaError_t launch_np(const I8GemmArgs& g, int num_sms, cudaStream_t stream) {
   const WaitTest wt = wait_test();
   p.wait_ns = wt.limit_ns; p.hold = wt.hold;
   auto kern = k_i8_few<NP, CTAS, BF16OUT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  static SmemOnce once;
+  cudaError_t e = once.set(kern, C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * ks));

@@ -1,6 +1,8 @@
 // tcgen05 wrappers of the 8-bit integer linear's kernels (kind::i8).
 #pragma once
 
+#include <atomic>
+
 #include "tcgen05.cuh"
 
 namespace nvfp4 {
@@ -92,6 +94,23 @@ __device__ __forceinline__ void copy_to_peer(uint32_t dst, uint32_t src, uint32_
                "r"(src), "r"(bytes), "r"(remote_bar)
                : "memory");
 }
+
+// A kernel's shared-memory limit, raised once per device (the call takes a
+// microsecond; for devices from the 64th on it is made every time).
+struct SmemOnce {
+  std::atomic<uint64_t> done{0};
+  template <typename F>
+  cudaError_t set(F kern, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit != 0 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
 
 // 2-D tensor map over int8 rows (rows x K, row pitch ld bytes): boxes of 128
 // bytes x box_rows rows, 128-byte swizzle, zero fill out of range.

@@ -141,7 +141,7 @@ struct LayerNormArgs {
 };
 cudaError_t launch_layernorm(const LayerNormArgs& n, int num_sms, cudaStream_t stream);
 // Rows of partial parameter gradients in the backward pass's workspace.
-constexpr int kLnMaxParts = 296;
+constexpr int kLnMaxParts = 160;     // at most one CTA per SM writes them
 int layernorm_parts(int64_t M);
 struct LayerNormBwdArgs {
   const void* dy; int64_t lddy; const void* x; int64_t ldx; nvfp4_dtype dt;

@@ -12,11 +12,13 @@
 
 #include "kernels.h"
 #include "rows.cuh"
-#include "tcgen05.cuh"
+#include "i8_tc.cuh"
 
 namespace nvfp4 {
 using namespace rows;
 namespace {
+
+constexpr int MAXT(int v) { return v <= 2 ? 1024 : v == 4 ? 640 : 512; }    // threads of a CTA, by registers per thread
 
 struct RowArgs {
   const void* x; int64_t ldx;
@@ -31,26 +33,22 @@ struct RowArgs {
   int* st;
 };
 
-template <typename P>
-__device__ __forceinline__ void affine8(float (&v)[8], const P* gamma, const P* beta, int64_t at) {
-  float t[8];
-  if (gamma != nullptr) {
-    fetch8(gamma + at, t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], t[i]);
-  }
-  if (beta != nullptr) {
-    fetch8(beta + at, t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __fadd_rn(v[i], t[i]);
-  }
-}
-
-// A team of warps per row; the row's units are held in registers, V per thread.
-// Rows longer than that go through in several chunks: each pass then reads
-// them again, the last chunk first (it is still in registers).
-template <typename T, typename P, bool NORM, bool QUANT, int V>
-__global__ void __launch_bounds__(1024) k_rows(const RowArgs a) {
+// A team of W warps per row; the row's units are held in registers, V per thread.
+// ONE: a row fits (units <= W * 32 * V).  The team then takes row after row, and
+// loads the next one before it works on the present one.  Otherwise rows go
+// through in several chunks, and each pass reads them again, the last chunk
+// first (it is still in registers).
+//
+// Bound: the quantizer alone by its bytes (8192 x 14336 bf16: 54 us, 6.6 TB/s).
+// With the norm, by the conversions to binary64 (two per element, 16 a cycle and
+// SM) and by instruction issue: 19 instructions per element, 45% issue slots used
+// (8192 x 4096 bf16: 37 us, where its bytes need 20.5).  Tried and not kept: two
+// rows per team (gain and bias read once: 41 us), rows and parameters staged in
+// shared memory with 1024 threads per SM (35 to 41 us), sums in fp32 (39 us, and
+// the codes would depend on the order).
+template <typename T, typename P, bool NORM, bool QUANT, int V, bool ONE>
+__global__ void __launch_bounds__(ONE ? MAXT(V) : 1024) k_rows(const RowArgs a) {
+  using Raw = Unit<T>;
   __shared__ double red_sum[2][kMaxWarps];
   __shared__ uint32_t red_max[2][kMaxWarps];
   Team team;
@@ -61,77 +59,119 @@ __global__ void __launch_bounds__(1024) k_rows(const RowArgs a) {
   const int teams = (blockDim.x >> 5) / a.warps;
   const int base = team.index * a.warps;
   const int t = team.warp * 32 + team.lane, span = a.warps * 32;
-  const int chunks = (a.units + span * V - 1) / (span * V);
+  const int chunks = ONE ? 1 : (a.units + span * V - 1) / (span * V);
   const double inv_k = 1.0 / (8.0 * (double)a.units);
+  const int64_t stride = (int64_t)gridDim.x * teams;
 
   tc::griddep_launch_dependents();
   tc::griddep_wait();
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * teams + team.index; row < a.M; row += (int64_t)gridDim.x * teams, turn ^= 1) {
+  Raw next[ONE ? V : 1];
+  auto fetch = [&](int64_t row) {
     const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (i * span + t < a.units) next[i].load(x, i * span + t, a.units);
+      else next[i].zero();
+    }
+  };
+  int64_t row = (int64_t)blockIdx.x * teams + team.index;
+  if constexpr (ONE) {
+    if (row < a.M) fetch(row);
+  }
+  for (; row < a.M; row += stride, turn ^= 1) {
     float v[V][8];
     auto load = [&](int c) {
+      const T* x = static_cast<const T*>(a.x) + row * a.ldx;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int u = (c * V + i) * span + t;
-        if (u < a.units) {
-          fetch8(x + (int64_t)u * 8, v[i]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-        }
+        Raw w;
+        if (u < a.units) w.load(x, u, a.units);
+        else w.zero();
+        w.unpack(v[i]);
       }
     };
+    if constexpr (ONE) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) next[i].unpack(v[i]);
+      if (row + stride < a.M) fetch(row + stride);
+    }
     float mean = 0.0f, rstd = 1.0f;
+    auto centre = [&](int c) {     // v = x - mean; zeros stay beyond the row's end
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if ((c * V + i) * span + t >= a.units) continue;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) add2(v[i][e], v[i][e + 1], -mean, -mean);
+      }
+    };
     if constexpr (NORM) {
-      double s = 0.0;
+      double s0 = 0.0, s1 = 0.0;                  // two chains
       for (int c = 0; c < chunks; ++c) {
-        load(c);
+        if (!ONE) load(c);
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) s += (double)v[i][e];
+          for (int e = 0; e < 8; e += 2) {
+            s0 += (double)v[i][e];
+            s1 += (double)v[i][e + 1];
+          }
       }
-      mean = (float)(team.sum(s, red_sum[0] + base) * inv_k);
-      double q = 0.0;
+      mean = (float)(team.sum(s0 + s1, red_sum[0] + base) * inv_k);
+      s0 = s1 = 0.0;
       for (int c = chunks - 1; c >= 0; --c) {
         if (c != chunks - 1) load(c);
+        centre(c);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if ((c * V + i) * span + t >= a.units) continue;
+        for (int i = 0; i < V; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const double d = (double)__fsub_rn(v[i][e], mean);
-            q = fma(d, d, q);
+          for (int e = 0; e < 8; e += 2) {
+            const double d0 = (double)v[i][e], d1 = (double)v[i][e + 1];
+            s0 = fma(d0, d0, s0);
+            s1 = fma(d1, d1, s1);
           }
-        }
       }
-      rstd = (float)(1.0 / sqrt(team.sum(q, red_sum[1] + base) * inv_k + (double)a.eps));
+      rstd = rsqrt_rounded(team.sum(s0 + s1, red_sum[1] + base) * inv_k + (double)a.eps);
       if (t == 0 && !(abs_key(mean) < 0x7F800000u && abs_key(rstd) < 0x7F800000u)) report_status(a.st, NVFP4_ERR_NONFINITE);
     }
-    // the row's result before its last rounding: v holds chunk c
+    // the row's result before its last rounding; v holds chunk c, as x - mean
     auto finish = [&](int c) {
       if constexpr (NORM) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int u = (c * V + i) * span + t;
           if (u >= a.units) continue;
+          float p[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[i][e] = __fmul_rn(__fsub_rn(v[i][e], mean), rstd);
-          affine8(v[i], static_cast<const P*>(a.gamma), static_cast<const P*>(a.beta), (int64_t)u * 8);
+          for (int e = 0; e < 8; e += 2) mul2(v[i][e], v[i][e + 1], rstd, rstd);
+          if (a.gamma != nullptr) {
+            Raw::param(static_cast<const P*>(a.gamma), u, a.units, p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i][e] = __fmul_rn(v[i][e], p[e]);
+          }
+          if (a.beta != nullptr) {
+            Raw::param(static_cast<const P*>(a.beta), u, a.units, p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i][e] = __fadd_rn(v[i][e], p[e]);
+          }
         }
       }
     };
-    // after the statistics pass chunk 0 is in registers; without one, nothing is
+    auto reload = [&](int c) {
+      load(c);
+      if constexpr (NORM) centre(c);
+    };
+    // after the statistics pass chunk 0 is in registers; without one (and not ONE), nothing is
     if constexpr (!QUANT) {
       T* y = static_cast<T*>(a.y) + row * a.ldy;
       for (int c = 0; c < chunks; ++c) {
-        if (c != 0) load(c);
+        if (c != 0) reload(c);
         finish(c);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int u = (c * V + i) * span + t;
-          if (u < a.units) store8(y + (int64_t)u * 8, v[i]);
+          if (u < a.units) Raw::store(y, u, a.units, v[i]);
         }
       }
       if (t == 0) {
@@ -139,17 +179,16 @@ __global__ void __launch_bounds__(1024) k_rows(const RowArgs a) {
         if (a.rstd != nullptr) a.rstd[row] = rstd;
       }
     } else {
-      uint32_t m = 0;
+      float top = 0.0f;
       for (int c = 0; c < chunks; ++c) {
-        if (!NORM || c != 0) load(c);
-        finish(c);
+        if ((!NORM && !ONE) || c != 0) reload(c);
+        finish(c);                 // what lies beyond the row's end is zero
 #pragma unroll
         for (int i = 0; i < V; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if ((c * V + i) * span + t < a.units) m = max(m, abs_key(v[i][e]));
+          for (int e = 0; e < 8; e += 2) top = max3_abs(top, v[i][e], v[i][e + 1]);
       }
-      m = team.max(m, red_max[turn] + base);
+      const uint32_t m = team.max(abs_key(top), red_max[turn] + base);
       const RowScale rs = row_scale(m);
       if (t == 0) {
         a.scales[row] = rs.scale;
@@ -159,46 +198,74 @@ __global__ void __launch_bounds__(1024) k_rows(const RowArgs a) {
       const bool zero = rs.inv == 0.0f;
       for (int c = chunks - 1; c >= 0; --c) {
         if (c != chunks - 1) {
-          load(c);
+          reload(c);
           finish(c);
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int u = (c * V + i) * span + t;
-          if (u < a.units)
-            *reinterpret_cast<uint2*>(codes + (int64_t)u * 8) = zero ? make_uint2(0u, 0u) : encode8(v[i], rs.inv);
+          if (u < a.units) Raw::store_codes(codes, u, a.units, zero ? make_uint2(0u, 0u) : encode8(v[i], rs.inv));
         }
       }
     }
   }
 }
 
-template <typename T, typename P, bool NORM, bool QUANT, int V>
-cudaError_t run_rows(const RowArgs& a, int threads, int grid, cudaStream_t stream) {
+cudaLaunchConfig_t dependent_launch(dim3 grid, int threads, size_t smem, cudaStream_t stream, cudaLaunchAttribute* at) {
+  at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at->val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_rows<T, P, NORM, QUANT, V>, a);
+  return cfg;
 }
 
-template <typename T, typename P, bool NORM, bool QUANT>
-cudaError_t launch_rows(RowArgs a, int num_sms, cudaStream_t stream) {
-  // few rows: one unit per thread, for latency; many: up to four, for bytes in flight per instruction
-  const int v = a.M <= num_sms ? 1 : (a.units > 1024 ? 4 : 2);
-  a.warps = std::min(kMaxWarps, (a.units + 32 * v - 1) / (32 * v));
-  const int teams = std::max(1, std::min({kMaxTeams, 8 / a.warps, kMaxWarps / a.warps}));
+template <typename T, typename P, bool NORM, bool QUANT, int V, bool ONE>
+cudaError_t run_rows(RowArgs a, int num_sms, cudaStream_t stream) {
+  auto kern = k_rows<T, P, NORM, QUANT, V, ONE>;
+  a.warps = ONE ? (a.units + 32 * V - 1) / (32 * V) : 32;
+  const int teams = std::max(1, 4 / a.warps), threads = 32 * a.warps * teams;
   const int64_t groups = (a.M + teams - 1) / teams;
-  const int grid = (int)std::min<int64_t>(groups, (int64_t)1 << 30);
-  const int threads = 32 * a.warps * teams;
-  if (v == 1) return run_rows<T, P, NORM, QUANT, 1>(a, threads, grid, stream);
-  if (v == 2) return run_rows<T, P, NORM, QUANT, 2>(a, threads, grid, stream);
-  return run_rows<T, P, NORM, QUANT, 4>(a, threads, grid, stream);
+  // persistent when rows fit: as many CTAs as are resident at once, by registers
+  // (8192 x 4096 bf16 with 1.6 waves of them instead: 43 us, 37 so)
+  static const int regs = [&] {
+    cudaFuncAttributes fa{};
+    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess && fa.numRegs > 0 ? fa.numRegs : 128;
+  }();
+  const int ctas = std::max(1, std::min(2048 / threads, 65536 / ((regs + 7) / 8 * 8 * threads)));
+  const int64_t grid = std::min<int64_t>(groups, ONE ? (int64_t)num_sms * ctas : (int64_t)1 << 30);
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = dependent_launch(dim3((unsigned)grid), threads, 0, stream, &at);
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+// Units per thread.  Many: fewer warps share a row's reductions, and a thread has
+// more bytes on their way (quantizer, 8192 x 14336 bf16: eight 54 us, four 67;
+// norm, 8192 x 8192 bf16: eight 68, four 77, two 86 us).  Few: more warps per row,
+// for latency and where rows are few (300 rows of 4096 into 8 bits: two 4.9,
+// four 5.7 us).  The norm holds shorter rows better in four units (5120 bf16: 44
+// us, eight 53) and fp32 in two (4096: 25.5, four 27.6 us); eight units of fp32
+// do not fit in registers.
+template <typename T, typename P, bool NORM, bool QUANT>
+cudaError_t launch_rows(const RowArgs& a, int num_sms, cudaStream_t stream) {
+  constexpr bool BF16 = sizeof(T) == 2;
+  auto fits = [&](int v) { return a.units <= MAXT(v) * v; };
+  int v = 4;
+  if (a.M <= num_sms) v = 1;
+  else if (NORM && a.M <= 3 * (int64_t)num_sms) v = 2;
+  else if (BF16) v = a.units >= (NORM ? 1024 : 512) ? 8 : 4;
+  else if (NORM) v = a.units <= 512 ? 2 : 4;
+  v = std::min(v, (a.units + 31) / 32);                // no more than fill a warp
+  if (v <= 1 && fits(1)) return run_rows<T, P, NORM, QUANT, 1, true>(a, num_sms, stream);
+  if (v <= 2 && fits(2)) return run_rows<T, P, NORM, QUANT, 2, true>(a, num_sms, stream);
+  if (v <= 4 && fits(4)) return run_rows<T, P, NORM, QUANT, 4, true>(a, num_sms, stream);
+  if constexpr (BF16)
+    if (fits(8)) return run_rows<T, P, NORM, QUANT, 8, true>(a, num_sms, stream);
+  return run_rows<T, P, NORM, QUANT, 4, false>(a, num_sms, stream);
 }
 
 template <bool NORM, bool QUANT>
@@ -216,10 +283,9 @@ cudaError_t launch_rows_typed(const RowArgs& a, nvfp4_dtype dt, nvfp4_dtype pdt,
 // One row, with xh = (x - mean) * rstd and g = dy * gamma:
 //   dx = rstd * (g - mean(g) - xh * mean(g * xh))
 // and, over all rows, dgamma = sum dy * xh, dbeta = sum dy.
-// A CTA takes the rows blockIdx.x, blockIdx.x + grid, ...; its threads keep the
-// running dgamma and dbeta of their own columns in registers and write them once,
-// as one row of the workspace.  k_ln_params then sums the grid's rows in a fixed
-// order, so results do not change from run to run.
+// The threads of a row keep the running dgamma and dbeta of their own columns in
+// registers over all rows they meet; a CTA writes them once, as one row of the
+// workspace, and k_ln_params sums those rows.  Every order of summation is fixed.
 struct BwdArgs {
   const void* dy; int64_t lddy;
   const void* x; int64_t ldx;
@@ -249,6 +315,189 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2* slot) {
   return v;
 }
 
+// A CTA of up to 512 threads works on `teams` rows at a time.  Each thread copies
+// its own units of x and dy into shared memory `stages` rows ahead (cp.async: a
+// thread waits for its own copies alone, so neither barriers nor registers are
+// spent on what is on its way), reads them once for the row's sums and the
+// parameters' gradients and once more for dx.  gamma waits in shared memory too:
+// from L1, which the ring leaves too small for it, 8192 x 8192 fp32 took 227 us.
+// Bound: bytes (8192 x 8192 fp32: 127 us, 6.35 TB/s; bf16: 88 us, where half the
+// bytes go with as many instructions).
+template <int N>
+__device__ __forceinline__ void copies_left() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+constexpr int kBwdThreads = 512, kBwdSmem = 224 * 1024, kBwdMaxStages = 4;
+
+template <typename T, typename P, int V>
+__global__ void __launch_bounds__(kBwdThreads, 1) k_ln_backward_rows(const BwdArgs a, int warps, int stages) {
+  using U = Unit<T>;
+  extern __shared__ __align__(16) uint8_t bwd_smem[];
+  float* gain = reinterpret_cast<float*>(bwd_smem);            // gamma, or ones
+  uint8_t* ring_raw = bwd_smem + (size_t)a.units * 32;
+  __shared__ float2 red[2][kMaxWarps];
+  Team team;
+  team.warps = warps;
+  team.index = (threadIdx.x >> 5) / warps;
+  team.warp = (threadIdx.x >> 5) - team.index * warps;
+  team.lane = threadIdx.x & 31;
+  const int teams = (blockDim.x >> 5) / warps, base = team.index * warps;
+  const int t = team.warp * 32 + team.lane, span = warps * 32;
+  const uint32_t row_bytes = (uint32_t)a.units * 8u * (uint32_t)sizeof(T);
+  uint8_t* ring = ring_raw + (size_t)team.index * stages * 2 * row_bytes;
+  const int64_t stride = (int64_t)gridDim.x * teams;
+  const float inv_k = 1.0f / (8.0f * (float)a.units);
+  float dg[V][8], db[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dg[i][e] = db[i][e] = 0.0f;
+  tc::griddep_launch_dependents();
+  tc::griddep_wait();
+  auto issue = [&](int64_t row, int stage) {
+    if (row < a.M) {
+      const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+      const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
+      const uint32_t dst = tc::saddr(ring + (size_t)stage * 2 * row_bytes);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int u = i * span + t;
+        if (u >= a.units) continue;
+#pragma unroll
+        for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
+          const uint32_t off = (uint32_t)(u + h * a.units) * 16u;
+          copy16(dst + off, reinterpret_cast<const uint8_t*>(x) + off);
+          copy16(dst + row_bytes + off, reinterpret_cast<const uint8_t*>(dy) + off);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const int64_t first = (int64_t)blockIdx.x * teams + team.index;
+  for (int s = 0; s < stages; ++s) issue(first + s * stride, s);
+  for (int u = threadIdx.x; u < a.units; u += blockDim.x) {
+    float v[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+    if (a.gamma != nullptr) U::param(static_cast<const P*>(a.gamma), u, a.units, v);
+    U::store_param(gain, u, a.units, v);
+  }
+  __syncthreads();
+  float mean = 0.0f, rstd = 0.0f;
+  if (first < a.M) { mean = a.mean[first]; rstd = a.rstd[first]; }
+  int turn = 0, stage = 0;
+  for (int64_t row = first; row < a.M; row += stride, turn ^= 1) {
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    if (row + stride < a.M) { next_mean = a.mean[row + stride]; next_rstd = a.rstd[row + stride]; }
+    if (stages == 4) copies_left<3>();
+    else if (stages == 3) copies_left<2>();
+    else copies_left<1>();
+    const T* xs = reinterpret_cast<const T*>(ring + (size_t)stage * 2 * row_bytes);
+    const T* ds = reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(xs) + row_bytes);
+    // xh and g = dy * gamma of unit u
+    auto unit = [&](int u, float (&xh)[8], float (&dyv)[8], float (&g)[8]) {
+      U w;
+      w.load(xs, u, a.units);
+      w.unpack(xh);
+      w.load(ds, u, a.units);
+      w.unpack(dyv);
+      U::param(gain, u, a.units, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        xh[e] = (xh[e] - mean) * rstd;
+        g[e] *= dyv[e];
+      }
+    };
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int u = i * span + t;
+      if (u >= a.units) continue;
+      float xh[8], dyv[8], g[8];
+      unit(u, xh, dyv, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s.x += g[e];
+        s.y = fmaf(g[e], xh[e], s.y);
+        dg[i][e] = fmaf(dyv[e], xh[e], dg[i][e]);
+        db[i][e] += dyv[e];
+      }
+    }
+    if (a.dx != nullptr) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, o);
+        s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, o);
+      }
+      if (warps > 1) {
+        float2* slot = red[turn] + base;
+        if (team.lane == 0) slot[team.warp] = s;
+        // one named barrier per team
+        asm volatile("bar.sync %0, %1;" ::"r"(team.index + 1), "r"(span) : "memory");
+        s = slot[0];
+        for (int w = 1; w < warps; ++w) {
+          s.x += slot[w].x;
+          s.y += slot[w].y;
+        }
+      }
+      const float c1 = s.x * inv_k, c2 = s.y * inv_k;
+      T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int u = i * span + t;
+        if (u >= a.units) continue;
+        float xh[8], dyv[8], g[8], o[8];
+        unit(u, xh, dyv, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = rstd * (g[e] - fmaf(xh[e], c2, c1));
+        U::store(dx, u, a.units, o);
+      }
+    }
+    issue(row + stages * stride, stage);
+    if (++stage == stages) stage = 0;
+    mean = next_mean;
+    rstd = next_rstd;
+  }
+  if (a.part == nullptr) return;
+  copies_left<0>();
+  float* pg = a.part + (int64_t)blockIdx.x * 16 * a.units;     // [dgamma | dbeta]
+  float* pb = pg + (int64_t)8 * a.units;
+  if (teams == 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int u = i * span + t;
+      if (u >= a.units) continue;
+      U::store_param(pg, u, a.units, dg[i]);
+      U::store_param(pb, u, a.units, db[i]);
+    }
+    return;
+  }
+  // the teams' sums, one after another, in the ring's place
+  float* sum = reinterpret_cast<float*>(ring_raw);
+  for (int k = 0; k < teams; ++k) {
+    __syncthreads();
+    if (team.index != k) continue;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int u = i * span + t;
+      if (u >= a.units) continue;
+      if (k > 0) {
+        float v[8];
+        U::param(sum, u, a.units, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dg[i][e] += v[e];
+        U::param(sum + a.units * 8, u, a.units, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) db[i][e] += v[e];
+      }
+      float* to_g = k == teams - 1 ? pg : sum;
+      float* to_b = k == teams - 1 ? pb : sum + a.units * 8;
+      U::store_param(to_g, u, a.units, dg[i]);
+      U::store_param(to_b, u, a.units, db[i]);
+    }
+  }
+}
+
+// Rows too long for that ring.
 // The rows' units beyond blockDim.x * V are taken in further column chunks
 // (blockIdx.y), each of which forms the row sums over the whole row again.
 template <typename T, typename P, int V>
@@ -272,10 +521,13 @@ __global__ void __launch_bounds__(512) k_ln_backward(const BwdArgs a) {
     float xh[V][8], g[V][8];
     float2 s = make_float2(0.0f, 0.0f);
     auto unit = [&](int u, float (&xv)[8], float (&gv)[8], float (&dyv)[8]) {
-      fetch8(x + (int64_t)u * 8, xv);
-      fetch8(dy + (int64_t)u * 8, dyv);
+      Unit<T> w;
+      w.load(x, u, a.units);
+      w.unpack(xv);
+      w.load(dy, u, a.units);
+      w.unpack(dyv);
       float gm[8];
-      if (a.gamma != nullptr) fetch8(static_cast<const P*>(a.gamma) + (int64_t)u * 8, gm);
+      if (a.gamma != nullptr) Unit<T>::param(static_cast<const P*>(a.gamma), u, a.units, gm);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         xv[e] = (xv[e] - mean) * rstd;
@@ -313,7 +565,7 @@ __global__ void __launch_bounds__(512) k_ln_backward(const BwdArgs a) {
         float o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = rstd * (g[i][e] - fmaf(xh[i][e], c2, c1));
-        store8(dx + (int64_t)u * 8, o);
+        Unit<T>::store(dx, u, a.units, o);
       }
     }
   }
@@ -324,45 +576,77 @@ __global__ void __launch_bounds__(512) k_ln_backward(const BwdArgs a) {
   for (int i = 0; i < V; ++i) {
     const int u = first + i * nt + t;
     if (u < a.units) {
-      store8(pg + (int64_t)u * 8, dg[i]);
-      store8(pb + (int64_t)u * 8, db[i]);
+      Unit<T>::store_param(pg, u, a.units, dg[i]);
+      Unit<T>::store_param(pb, u, a.units, db[i]);
     }
   }
 }
 
 // dgamma / dbeta = sum over the workspace's rows: 32 columns per CTA, one warp
-// per group of rows, joined in shared memory in the order of the warps.
-__global__ void __launch_bounds__(256) k_ln_params(const float* part, int parts, int64_t K, float* dgamma,
-                                                   float* dbeta) {
-  __shared__ float red[8][33];
+// per 32nd row, joined in shared memory in the order of the warps.
+__global__ void __launch_bounds__(1024) k_ln_params(const float* part, int parts, int64_t K, float* dgamma,
+                                                    float* dbeta) {
+  __shared__ float red[32][33];
   const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  const int64_t c = (int64_t)blockIdx.x * 32 + l;   // column of [dgamma | dbeta]
+  const int64_t c = (int64_t)blockIdx.x * 32 + l;   // column of [dgamma | dbeta]; 2 K is a multiple of 32
   tc::griddep_launch_dependents();
   tc::griddep_wait();
+  float v[(kLnMaxParts + 31) / 32];
+#pragma unroll
+  for (int i = 0; i < (kLnMaxParts + 31) / 32; ++i)
+    v[i] = w + 32 * i < parts ? part[(int64_t)(w + 32 * i) * 2 * K + c] : 0.0f;
   float s = 0.0f;
-  if (c < 2 * K)
-    for (int r = w; r < parts; r += 8) s += part[(int64_t)r * 2 * K + c];
+#pragma unroll
+  for (int i = 0; i < (kLnMaxParts + 31) / 32; ++i) s += v[i];
   red[w][l] = s;
   __syncthreads();
-  if (w == 0 && c < 2 * K) {
+  if (w == 0) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][l];
+    for (int i = 1; i < 32; ++i) s += red[i][l];
     float* out = c < K ? dgamma : dbeta;
     if (out != nullptr) out[c < K ? c : c - K] = s;
   }
 }
 
+template <typename T, typename P, int V>
+cudaError_t run_backward_rows(const BwdArgs& a, int warps, int teams, int stages, int parts, cudaStream_t stream) {
+  static tc::SmemOnce once;
+  cudaError_t e = once.set(k_ln_backward_rows<T, P, V>, kBwdSmem);
+  if (e != cudaSuccess) return e;
+  const size_t row = (size_t)a.units * 8 * sizeof(T), sums = teams > 1 ? (size_t)a.units * 64 : 0;
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = dependent_launch(dim3((unsigned)parts), 32 * warps * teams,
+                                                  (size_t)a.units * 32 + std::max((size_t)teams * stages * 2 * row, sums), stream, &at);
+  return cudaLaunchKernelEx(&cfg, k_ln_backward_rows<T, P, V>, a, warps, stages);
+}
+
+// *parts: rows of the workspace that were written.
 template <typename T, typename P>
-cudaError_t run_backward(const BwdArgs& a, dim3 grid, int threads, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+cudaError_t run_backward(const BwdArgs& a, int num_sms, int* parts, cudaStream_t stream) {
+  const int most = std::min(num_sms, kLnMaxParts);
+  // Units per thread: few rows, more threads on each (64 x 4096 bf16: one 7.1 us,
+  // two 8.1, four 10.1; 333 x 5120: two 12.2, four 12.6); many, more rows at a time
+  // (8192 x 8192 bf16: four 88 us, two 106), unless a row is short (1024: four 23
+  // us, two 19).  Halved until a team's rows fit in shared memory twice.
+  int v = a.M <= num_sms ? 1 : a.M <= 4 * (int64_t)num_sms || a.units < 256 ? 2 : 4;
+  while (v < 4 && (a.units + 32 * v - 1) / (32 * v) > kBwdThreads / 32) v *= 2;
+  for (; v >= 1; v /= 2) {
+    const int warps = (a.units + 32 * v - 1) / (32 * v);
+    if (warps > kBwdThreads / 32) break;
+    const int teams = std::min(kBwdThreads / 32 / warps, 15);
+    const int64_t per_stage = (int64_t)teams * 2 * a.units * 8 * (int64_t)sizeof(T);
+    const int stages = (int)std::min<int64_t>(kBwdMaxStages, (kBwdSmem - (int64_t)a.units * 32) / per_stage);
+    if (stages < 2) continue;
+    *parts = (int)std::min<int64_t>(most, (a.M + teams - 1) / teams);
+    if (v == 4) return run_backward_rows<T, P, 4>(a, warps, teams, stages, *parts, stream);
+    if (v == 2) return run_backward_rows<T, P, 2>(a, warps, teams, stages, *parts, stream);
+    return run_backward_rows<T, P, 1>(a, warps, teams, stages, *parts, stream);
+  }
+  const int threads = std::min(512, (a.units + 63) / 64 * 32);
+  *parts = (int)std::min<int64_t>(most, a.M);
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = dependent_launch(
+      dim3((unsigned)*parts, (unsigned)((a.units + 2 * threads - 1) / (2 * threads))), threads, 0, stream, &at);
   return cudaLaunchKernelEx(&cfg, k_ln_backward<T, P, 2>, a);
 }
 
@@ -389,33 +673,23 @@ cudaError_t launch_layernorm(const LayerNormArgs& n, int num_sms, cudaStream_t s
 int layernorm_parts(int64_t M) { return (int)std::min<int64_t>(M, kLnMaxParts); }
 
 cudaError_t launch_layernorm_backward(const LayerNormBwdArgs& n, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
   BwdArgs a{};
   a.dy = n.dy; a.lddy = n.lddy; a.x = n.x; a.ldx = n.ldx; a.gamma = n.gamma;
   a.mean = n.mean; a.rstd = n.rstd; a.dx = n.dx; a.lddx = n.lddx;
   const bool params = n.dgamma != nullptr || n.dbeta != nullptr;
   a.part = params ? n.part : nullptr;
   a.M = n.M; a.units = (int)(n.K / 8);
-  const int parts = layernorm_parts(n.M);
-  const int threads = std::min(512, (a.units + 63) / 64 * 32);
-  const dim3 grid((unsigned)parts, (unsigned)((a.units + 2 * threads - 1) / (2 * threads)));
+  int parts = 0;
   cudaError_t e;
   if (n.dt == NVFP4_BF16)
-    e = n.pdt == NVFP4_BF16 ? run_backward<__nv_bfloat16, __nv_bfloat16>(a, grid, threads, stream)
-                            : run_backward<__nv_bfloat16, float>(a, grid, threads, stream);
+    e = n.pdt == NVFP4_BF16 ? run_backward<__nv_bfloat16, __nv_bfloat16>(a, num_sms, &parts, stream)
+                            : run_backward<__nv_bfloat16, float>(a, num_sms, &parts, stream);
   else
-    e = n.pdt == NVFP4_BF16 ? run_backward<float, __nv_bfloat16>(a, grid, threads, stream)
-                            : run_backward<float, float>(a, grid, threads, stream);
+    e = n.pdt == NVFP4_BF16 ? run_backward<float, __nv_bfloat16>(a, num_sms, &parts, stream)
+                            : run_backward<float, float>(a, num_sms, &parts, stream);
   if (e != cudaSuccess || !params) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((2 * n.K + 31) / 32));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = dependent_launch(dim3((unsigned)(2 * n.K / 32)), 1024, 0, stream, &at);
   return cudaLaunchKernelEx(&cfg, k_ln_params, (const float*)a.part, parts, n.K, n.dgamma, n.dbeta);
 }
 
