@@ -208,8 +208,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (elect_one()) commit<CG>(saddr(mma_drain));
     __syncwarp();
     (void)mbar_drain<CG == 2>(saddr(mma_drain), 0u, ws, p.st);
-  } else if (CG == 2 && warp == 1) {
-    (void)mbar_drain<true>(saddr(mma_drain), 0u, ws, p.st);   // the leader's last commit has arrived here too
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - 4) >> 2, et = threadIdx.x - 128;
@@ -302,6 +300,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   if constexpr (CG == 2) cluster_sync();   // the pair's MMAs and arrivals are over before either CTA leaves
   else __syncthreads();
   if (warp == 1) {
+    // the leader's last commit, issued before it came here, arrives in the other CTA too
+    if (CG == 2 && rank != 0) (void)mbar_drain<true>(saddr(mma_drain), 0u, ws, p.st);
+    __syncwarp();
     tc_fence_after();
     if constexpr (CG == 2)
       asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 template <int CG>
 cudaError_t launch_tiles(const I8GemmArgs& g, int bn, int num_sms, cudaStream_t stream) {
   const int64_t mb = (g.M + BM * CG - 1) / (BM * CG), nb = (g.N + bn - 1) / bn;
-  if (mb * nb > INT32_MAX) return cudaErrorNotSupported;    // 32-bit tile numbers
+  if (mb * nb > INT32_MAX - 4096) return cudaErrorNotSupported;    // 32-bit tile numbers, one grid beyond the last
   CUtensorMap tmA, tmB;
   if (!encode_i8_map(&tmA, g.a, g.M, g.K, g.lda, BM) ||
       !encode_i8_map(&tmB, g.w, g.N, g.K, g.ldw, (uint32_t)(bn / CG)))

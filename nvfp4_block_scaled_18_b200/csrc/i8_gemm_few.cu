@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr int G = C::G;
   const int T = p.per_owner, groups = (p.M + G - 1) / G;       // G tokens each
   const int own0 = min(groups, rank * T / G), own1 = min(groups, (rank + 1) * T / G);
+  bool arrived = true;
   if (ks > 1) {
     if (threadIdx.x == 0) {
       const int bytes = (ks - 1) * (own1 - own0) * G * 512;
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     __syncwarp();
-    (void)warp_wait<true, true>(saddr(landed), 0u, ws, p.st);
+    arrived = warp_wait<true, true>(saddr(landed), 0u, ws, p.st);
     cluster_arrive();                // what this CTA was sent is here: the senders may leave
   } else {
     __syncthreads();                 // token_scale
@@ -249,7 +250,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
   }
-  if (ks > 1) cluster_wait();        // what this CTA sent has arrived
+  if (ks > 1) {
+    cluster_wait();                  // what this CTA sent has arrived
+    if (!arrived) (void)warp_wait<true, true>(saddr(landed), 0u, ws, p.st);    // given up before: all has been sent by now
+  }
 }
 
 // The largest split of K whose clusters fit one wave (whole clusters in GPCs of
