@@ -34,19 +34,19 @@ struct RowArgs {
 };
 
 // A team of W warps per row; the row's units are held in registers, V per thread.
+// FULL: every thread has V units.
 // ONE: a row fits (units <= W * 32 * V).  The team then takes row after row, and
 // loads the next one before it works on the present one.  Otherwise rows go
 // through in several chunks, and each pass reads them again, the last chunk
 // first (it is still in registers).
 //
 // Bound: the quantizer alone by its bytes (8192 x 14336 bf16: 54 us, 6.6 TB/s).
-// With the norm, by the conversions to binary64 (two per element, 16 a cycle and
-// SM) and by instruction issue: 19 instructions per element, 45% issue slots used
-// (8192 x 4096 bf16: 37 us, where its bytes need 20.5).  Tried and not kept: two
-// rows per team (gain and bias read once: 41 us), rows and parameters staged in
-// shared memory with 1024 threads per SM (35 to 41 us), sums in fp32 (39 us, and
-// the codes would depend on the order).
-template <typename T, typename P, bool NORM, bool QUANT, int V, bool ONE>
+// With the norm, by instruction issue, 19 instructions per element: of 37 us for
+// 8192 x 4096 bf16 with fp32 parameters the row's two reductions take 9, the gain
+// and the bias 10 and binary64 3 (2048 x 4096 into 8 bits: 12 us).  Tried and not
+// kept: two rows per team (41 us), and sums in fp32, whose codes would depend on
+// the order.
+template <typename T, typename P, bool NORM, bool QUANT, int V, bool ONE, bool FULL>
 __global__ void __launch_bounds__(ONE ? MAXT(V) : 1024) k_rows(const RowArgs a) {
   using Raw = Unit<T>;
   __shared__ double red_sum[2][kMaxWarps];
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(ONE ? MAXT(V) : 1024) k_rows(const RowArgs a) 
     const T* x = static_cast<const T*>(a.x) + row * a.ldx;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      if (i * span + t < a.units) next[i].load(x, i * span + t, a.units);
+      if (FULL || i * span + t < a.units) next[i].load(x, i * span + t, a.units);
       else next[i].zero();
     }
   };
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(ONE ? MAXT(V) : 1024) k_rows(const RowArgs a) 
       for (int i = 0; i < V; ++i) {
         const int u = (c * V + i) * span + t;
         Raw w;
-        if (u < a.units) w.load(x, u, a.units);
+        if (FULL || u < a.units) w.load(x, u, a.units);
         else w.zero();
         w.unpack(v[i]);
       }
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(ONE ? MAXT(V) : 1024) k_rows(const RowArgs a) 
     auto centre = [&](int c) {     // v = x - mean; zeros stay beyond the row's end
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if ((c * V + i) * span + t >= a.units) continue;
+        if (!FULL && (c * V + i) * span + t >= a.units) continue;
 #pragma unroll
         for (int e = 0; e < 8; e += 2) add2(v[i][e], v[i][e + 1], -mean, -mean);
       }
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(ONE ? MAXT(V) : 1024) k_rows(const RowArgs a) 
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int u = (c * V + i) * span + t;
-          if (u >= a.units) continue;
+          if (!FULL && u >= a.units) continue;
           float p[8];
 #pragma unroll
           for (int e = 0; e < 8; e += 2) mul2(v[i][e], v[i][e + 1], rstd, rstd);
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(ONE ? MAXT(V) : 1024) k_rows(const RowArgs a) 
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int u = (c * V + i) * span + t;
-          if (u < a.units) Raw::store(y, u, a.units, v[i]);
+          if (FULL || u < a.units) Raw::store(y, u, a.units, v[i]);
         }
       }
       if (t == 0) {
@@ -204,11 +204,181 @@ __global__ void __launch_bounds__(ONE ? MAXT(V) : 1024) k_rows(const RowArgs a) 
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const int u = (c * V + i) * span + t;
-          if (u < a.units) Raw::store_codes(codes, u, a.units, zero ? make_uint2(0u, 0u) : encode8(v[i], rs.inv));
+          if (FULL || u < a.units) Raw::store_codes(codes, u, a.units, zero ? make_uint2(0u, 0u) : encode8(v[i], rs.inv));
         }
       }
     }
   }
+}
+
+template <int N>
+__device__ __forceinline__ void copies_left() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Layer norm of many long rows: the steps of k_rows with fewer warps per row (two
+// for 4096 elements), since a row's reductions cost every one of its warps some
+// hundred instructions and a barrier.  A thread holds V units as they are in
+// memory and unpacks them for each pass; the next row arrives meanwhile in the
+// thread's own part of shared memory (cp.async: it waits for its own copies
+// alone).  Gain and bias are in shared memory as fp32, laid out for loads of whole
+// lines.  Bound: instruction issue and the conversions to binary64 still (8192 x
+// 4096 bf16 with fp32 parameters: 31 us, its bytes 20.5; 8192 x 8192: 57 and 41;
+// 4096 x 4096 fp32: 25 and 20.5).  Sixteen units a thread, one warp a row, spill:
+// 58 us.
+constexpr int kNormThreads = 512, kNormSmem = 224 * 1024;
+
+template <typename T, typename P, bool QUANT, int V, bool FULL>
+__global__ void __launch_bounds__(kNormThreads, 1) k_norm_rows(const RowArgs a) {
+  using U = Unit<T>;
+  extern __shared__ __align__(16) uint8_t norm_smem[];
+  float* gain = reinterpret_cast<float*>(norm_smem);     // elements 0-3 of every unit, then 4-7
+  float* bias = gain + a.units * 8;
+  __shared__ double red_sum[2][kNormThreads / 32];
+  __shared__ uint32_t red_max[2][kNormThreads / 32];
+  const int warps = a.warps, index = (threadIdx.x >> 5) / warps, lane = threadIdx.x & 31;
+  const int warp = (threadIdx.x >> 5) - index * warps;
+  const int teams = (blockDim.x >> 5) / warps, base = index * warps, span = warps * 32, t = warp * 32 + lane;
+  const uint32_t row_bytes = (uint32_t)a.units * 8u * (uint32_t)sizeof(T);
+  const uint8_t* stage = norm_smem + (uint32_t)a.units * 64u + (uint32_t)index * row_bytes;
+  const int64_t stride = (int64_t)gridDim.x * teams, first = (int64_t)blockIdx.x * teams + index;
+  const double inv_k = 1.0 / (8.0 * (double)a.units);
+  tc::griddep_launch_dependents();
+  tc::griddep_wait();
+  auto issue = [&](int64_t row) {
+    if (row < a.M) {
+      const uint8_t* x = reinterpret_cast<const uint8_t*>(static_cast<const T*>(a.x) + row * a.ldx);
+      const uint32_t dst = tc::saddr(stage);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int u = i * span + t;
+        if (!FULL && u >= a.units) continue;
+#pragma unroll
+        for (int h = 0; h < (int)sizeof(T) / 2; ++h) {
+          const uint32_t off = (uint32_t)(u + h * a.units) * 16u;
+          copy16(dst + off, x + off);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  issue(first);
+  for (int u = threadIdx.x; u < a.units; u += blockDim.x) {
+    float g[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f}, b[8] = {};
+    if (a.gamma != nullptr) U::param(static_cast<const P*>(a.gamma), u, a.units, g);
+    if (a.beta != nullptr) U::param(static_cast<const P*>(a.beta), u, a.units, b);
+    Unit<float>::store(gain, u, a.units, g);
+    Unit<float>::store(bias, u, a.units, b);
+  }
+  __syncthreads();
+  auto sync = [&] { asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(span) : "memory"); };
+  auto total = [&](double x, double* slot) {
+    x = warp_sum_f64(x);
+    if (warps == 1) return x;
+    if (lane == 0) slot[warp] = x;
+    sync();
+    x = slot[0];
+    for (int w = 1; w < warps; ++w) x += slot[w];
+    return x;
+  };
+  int turn = 0;
+  for (int64_t row = first; row < a.M; row += stride, turn ^= 1) {
+    copies_left<0>();
+    U held[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int u = i * span + t;
+      if (FULL || u < a.units) held[i].load(reinterpret_cast<const T*>(stage), u, a.units);
+      else held[i].zero();
+    }
+    double s[4] = {0.0, 0.0, 0.0, 0.0};                   // chains
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float v[8];
+      held[i].unpack(v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e & 3] += (double)v[e];
+    }
+    issue(row + stride);                                  // the row has been read
+    const float mean = (float)(total((s[0] + s[1]) + (s[2] + s[3]), red_sum[0] + base) * inv_k);
+    s[0] = s[1] = s[2] = s[3] = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      held[i].forget();
+      if (!FULL && i * span + t >= a.units) continue;
+      float v[8];
+      held[i].unpack(v);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        add2(v[e], v[e + 1], -mean, -mean);
+        const double d0 = (double)v[e], d1 = (double)v[e + 1];
+        s[e & 3] = fma(d0, d0, s[e & 3]);
+        s[(e + 1) & 3] = fma(d1, d1, s[(e + 1) & 3]);
+      }
+    }
+    const float rstd =
+        rsqrt_rounded(total((s[0] + s[1]) + (s[2] + s[3]), red_sum[1] + base) * inv_k + (double)a.eps);
+    if (t == 0 && !(abs_key(mean) < 0x7F800000u && abs_key(rstd) < 0x7F800000u)) report_status(a.st, NVFP4_ERR_NONFINITE);
+    auto result = [&](int i, float (&v)[8]) {             // before its last rounding
+      const int u = i * span + t;
+      float p[8];
+      held[i].forget();
+      held[i].unpack(v);
+      Unit<float>::param(gain, u, a.units, p);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        add2(v[e], v[e + 1], -mean, -mean);
+        mul2(v[e], v[e + 1], rstd, rstd);
+        v[e] = __fmul_rn(v[e], p[e]);
+        v[e + 1] = __fmul_rn(v[e + 1], p[e + 1]);
+      }
+      Unit<float>::param(bias, u, a.units, p);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __fadd_rn(v[e], p[e]);
+    };
+    if constexpr (!QUANT) {
+      T* y = static_cast<T*>(a.y) + row * a.ldy;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (!FULL && i * span + t >= a.units) continue;
+        float v[8];
+        result(i, v);
+        U::store(y, i * span + t, a.units, v);
+      }
+      if (t == 0) {
+        if (a.mean != nullptr) a.mean[row] = mean;
+        if (a.rstd != nullptr) a.rstd[row] = rstd;
+      }
+    } else {
+      float top = 0.0f, v[V][8];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (!FULL && i * span + t >= a.units) continue;
+        result(i, v[i]);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) top = max3_abs(top, v[i][e], v[i][e + 1]);
+      }
+      uint32_t m = __reduce_max_sync(0xFFFFFFFFu, abs_key(top));
+      if (warps > 1) {
+        if (lane == 0) red_max[turn][base + warp] = m;
+        sync();
+        m = __reduce_max_sync(0xFFFFFFFFu, lane < warps ? red_max[turn][base + lane] : 0u);
+      }
+      const RowScale rs = row_scale(m);
+      if (t == 0) {
+        a.scales[row] = rs.scale;
+        if (m >= 0x7F800000u) report_status(a.st, NVFP4_ERR_NONFINITE);
+      }
+      int8_t* codes = a.codes + row * a.ldc;
+      const bool zero = rs.inv == 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if (!FULL && i * span + t >= a.units) continue;
+        U::store_codes(codes, i * span + t, a.units, zero ? make_uint2(0u, 0u) : encode8(v[i], rs.inv));
+      }
+    }
+  }
+  copies_left<0>();
 }
 
 cudaLaunchConfig_t dependent_launch(dim3 grid, int threads, size_t smem, cudaStream_t stream, cudaLaunchAttribute* at) {
@@ -224,9 +394,11 @@ cudaLaunchConfig_t dependent_launch(dim3 grid, int threads, size_t smem, cudaStr
   return cfg;
 }
 
-template <typename T, typename P, bool NORM, bool QUANT, int V, bool ONE>
+template <typename T, typename P, bool NORM, bool QUANT, int V, bool ONE, bool FULL = false>
 cudaError_t run_rows(RowArgs a, int num_sms, cudaStream_t stream) {
-  auto kern = k_rows<T, P, NORM, QUANT, V, ONE>;
+  if constexpr (ONE && !FULL)
+    if (a.units % (32 * V) == 0) return run_rows<T, P, NORM, QUANT, V, ONE, true>(a, num_sms, stream);
+  auto kern = k_rows<T, P, NORM, QUANT, V, ONE, FULL>;
   a.warps = ONE ? (a.units + 32 * V - 1) / (32 * V) : 32;
   const int teams = std::max(1, 4 / a.warps), threads = 32 * a.warps * teams;
   const int64_t groups = (a.M + teams - 1) / teams;
@@ -243,6 +415,33 @@ cudaError_t run_rows(RowArgs a, int num_sms, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+template <typename T, typename P, bool QUANT, int V, bool FULL = false>
+cudaError_t run_norm_rows(RowArgs a, int num_sms, cudaStream_t stream) {
+  if constexpr (!FULL)
+    if (a.units % (32 * V) == 0) return run_norm_rows<T, P, QUANT, V, true>(a, num_sms, stream);
+  a.warps = (a.units + 32 * V - 1) / (32 * V);
+  if (a.warps > kNormThreads / 32) return cudaErrorNotSupported;
+  const int64_t row = (int64_t)a.units * 8 * (int64_t)sizeof(T), params = (int64_t)a.units * 64;
+  const int teams = (int)std::min<int64_t>({kNormThreads / 32 / a.warps, a.warps == 1 ? 16 : 15, (kNormSmem - params) / row});
+  if (teams < 1) return cudaErrorNotSupported;
+  static tc::SmemOnce once;
+  const cudaError_t e = once.set(k_norm_rows<T, P, QUANT, V, FULL>, kNormSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = std::min<int64_t>((a.M + teams - 1) / teams, num_sms);
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg =
+      dependent_launch(dim3((unsigned)grid), 32 * a.warps * teams, (size_t)(params + teams * row), stream, &at);
+  return cudaLaunchKernelEx(&cfg, k_norm_rows<T, P, QUANT, V, FULL>, a);
+}
+
+// Ten or five units per thread if that leaves none idle and eight does not.
+template <typename T, typename P, bool QUANT>
+cudaError_t launch_norm_rows(const RowArgs& a, int num_sms, cudaStream_t stream) {
+  if (a.units % 256 != 0 && !QUANT && a.units % 320 == 0) return run_norm_rows<T, P, QUANT, 10>(a, num_sms, stream);
+  if (a.units % 256 != 0 && a.units % 160 == 0) return run_norm_rows<T, P, QUANT, 5>(a, num_sms, stream);
+  return run_norm_rows<T, P, QUANT, 8>(a, num_sms, stream);
+}
+
 // Units per thread.  Many: fewer warps share a row's reductions, and a thread has
 // more bytes on their way (quantizer, 8192 x 14336 bf16: eight 54 us, four 67;
 // norm, 8192 x 8192 bf16: eight 68, four 77, two 86 us).  Few: more warps per row,
@@ -254,6 +453,15 @@ template <typename T, typename P, bool NORM, bool QUANT>
 cudaError_t launch_rows(const RowArgs& a, int num_sms, cudaStream_t stream) {
   constexpr bool BF16 = sizeof(T) == 2;
   auto fits = [&](int v) { return a.units <= MAXT(v) * v; };
+  // k_norm_rows: from 16 KB a row on (4800 x 8192 bf16: 39 us, k_rows 44; into 8 bits
+  // 44 and 50; 4800 x 4096 bf16: 22.8 and 19.5), and where k_rows would read fp32
+  // parameters beside bf16 rows, two lines a load (8192 x 4096: 31 and 37 us).
+  const int64_t row_bytes = (int64_t)a.units * 8 * (int64_t)sizeof(T);
+  if constexpr (NORM)
+    if (a.M > 3 * (int64_t)num_sms && (row_bytes >= 16384 || (sizeof(P) > sizeof(T) && row_bytes >= 8192 && a.M >= 4096))) {
+      const cudaError_t e = launch_norm_rows<T, P, QUANT>(a, num_sms, stream);
+      if (e != cudaErrorNotSupported) return e;
+    }
   int v = 4;
   if (a.M <= num_sms) v = 1;
   else if (NORM && a.M <= 3 * (int64_t)num_sms) v = 2;
@@ -323,11 +531,6 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2* slot) {
 // from L1, which the ring leaves too small for it, 8192 x 8192 fp32 took 227 us.
 // Bound: bytes (8192 x 8192 fp32: 127 us, 6.35 TB/s; bf16: 88 us, where half the
 // bytes go with as many instructions).
-template <int N>
-__device__ __forceinline__ void copies_left() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 constexpr int kBwdThreads = 512, kBwdSmem = 224 * 1024, kBwdMaxStages = 4;
 
 template <typename T, typename P, int V>

@@ -96,53 +96,68 @@ __device__ __forceinline__ void unpack8(const float4& a, const float4& b, float 
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
+// Element i of an array of V, by a 32-bit byte offset from a uniform base.
+template <typename V, typename B>
+__device__ __forceinline__ const V& at(const B* base, int i) {
+  return *reinterpret_cast<const V*>(reinterpret_cast<const char*>(base) + (uint32_t)i * (uint32_t)sizeof(V));
+}
+template <typename V, typename B>
+__device__ __forceinline__ V& at(B* base, int i) {
+  return *reinterpret_cast<V*>(reinterpret_cast<char*>(base) + (uint32_t)i * (uint32_t)sizeof(V));
+}
+
 template <typename T> struct Unit;
 template <> struct Unit<__nv_bfloat16> {
   using T = __nv_bfloat16;
   uint4 w;                       // as it is in memory: what a row on its way occupies
-  __device__ __forceinline__ void load(const T* row, int u, int) { w = reinterpret_cast<const uint4*>(row)[u]; }
+  __device__ __forceinline__ void load(const T* row, int u, int) { w = at<uint4>(row, u); }
   __device__ __forceinline__ void zero() { w = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void unpack(float (&v)[8]) const { unpack8(w, v); }
+  // unpacked again after this, not kept unpacked
+  __device__ __forceinline__ void forget() { asm volatile("" : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w)); }
   static __device__ __forceinline__ void store(T* row, int u, int, const float (&v)[8]) {
-    reinterpret_cast<uint4*>(row)[u] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+    at<uint4>(row, u) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
                                                   pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
   }
-  static __device__ __forceinline__ void store_codes(int8_t* row, int u, int, uint2 c) { reinterpret_cast<uint2*>(row)[u] = c; }
+  static __device__ __forceinline__ void store_codes(int8_t* row, int u, int, uint2 c) { at<uint2>(row, u) = c; }
   // the unit's elements of a parameter vector
   static __device__ __forceinline__ void param(const __nv_bfloat16* p, int u, int, float (&v)[8]) {
-    unpack8(reinterpret_cast<const uint4*>(p)[u], v);
+    unpack8(at<uint4>(p, u), v);
   }
   static __device__ __forceinline__ void param(const float* p, int u, int, float (&v)[8]) {
-    unpack8(reinterpret_cast<const float4*>(p)[2 * u], reinterpret_cast<const float4*>(p)[2 * u + 1], v);
+    unpack8(at<float4>(p, 2 * u), at<float4>(p, 2 * u + 1), v);
   }
   static __device__ __forceinline__ void store_param(float* p, int u, int, const float (&v)[8]) {
-    reinterpret_cast<float4*>(p)[2 * u] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(p)[2 * u + 1] = make_float4(v[4], v[5], v[6], v[7]);
+    at<float4>(p, 2 * u) = make_float4(v[0], v[1], v[2], v[3]);
+    at<float4>(p, 2 * u + 1) = make_float4(v[4], v[5], v[6], v[7]);
   }
 };
 template <> struct Unit<float> {
   using T = float;
   float4 a, b;
   __device__ __forceinline__ void load(const T* row, int u, int units) {
-    a = reinterpret_cast<const float4*>(row)[u];
-    b = reinterpret_cast<const float4*>(row)[u + units];
+    a = at<float4>(row, u);
+    b = at<float4>(row, u + units);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
   __device__ __forceinline__ void unpack(float (&v)[8]) const { unpack8(a, b, v); }
+  __device__ __forceinline__ void forget() {
+    asm volatile("" : "+f"(a.x), "+f"(a.y), "+f"(a.z), "+f"(a.w), "+f"(b.x), "+f"(b.y), "+f"(b.z), "+f"(b.w));
+  }
   static __device__ __forceinline__ void store(T* row, int u, int units, const float (&v)[8]) {
-    reinterpret_cast<float4*>(row)[u] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4*>(row)[u + units] = make_float4(v[4], v[5], v[6], v[7]);
+    at<float4>(row, u) = make_float4(v[0], v[1], v[2], v[3]);
+    at<float4>(row, u + units) = make_float4(v[4], v[5], v[6], v[7]);
   }
   static __device__ __forceinline__ void store_codes(int8_t* row, int u, int units, uint2 c) {
-    reinterpret_cast<uint32_t*>(row)[u] = c.x;
-    reinterpret_cast<uint32_t*>(row)[u + units] = c.y;
+    at<uint32_t>(row, u) = c.x;
+    at<uint32_t>(row, u + units) = c.y;
   }
   static __device__ __forceinline__ void param(const __nv_bfloat16* p, int u, int units, float (&v)[8]) {
-    const uint2 x = reinterpret_cast<const uint2*>(p)[u], y = reinterpret_cast<const uint2*>(p)[u + units];
+    const uint2 x = at<uint2>(p, u), y = at<uint2>(p, u + units);
     unpack8(make_uint4(x.x, x.y, y.x, y.y), v);
   }
   static __device__ __forceinline__ void param(const float* p, int u, int units, float (&v)[8]) {
-    unpack8(reinterpret_cast<const float4*>(p)[u], reinterpret_cast<const float4*>(p)[u + units], v);
+    unpack8(at<float4>(p, u), at<float4>(p, u + units), v);
   }
   static __device__ __forceinline__ void store_param(float* p, int u, int units, const float (&v)[8]) { store(p, u, units, v); }
 };

@@ -40,7 +40,7 @@ def status():
 
 
 SIZES = [(1, 16), (3, 48), (5, 256), (1, 4096), (149, 1008), (7, 8192), (33, 8208), (3, 14336), (2, 33040), (300, 5120),
-         (1, 131056)]
+         (1, 131056), (446, 5120), (460, 8192), (450, 10240), (445, 14352), (4100, 4096)]
 
 
 @pytest.mark.parametrize("rows,cols", SIZES)
