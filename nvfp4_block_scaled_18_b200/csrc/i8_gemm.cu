@@ -21,6 +21,7 @@
 //              epilogue runs under the next tile's MMAs.
 // Every mbarrier wait is bounded, as in the other tensor-core kernels.
 #include <algorithm>
+#include <type_traits>
 
 #include "i8_tc.cuh"
 #include "kernels.h"
@@ -55,10 +56,11 @@ struct Params {
   void* y;
   int64_t ldy;
   int y_vec;          // Y's base and row pitch allow 16-byte stores
-  int M, N, K;
+  int M, N, K;        // of the tiles: SWAP has the channels as M and the tokens as N
   int bn;             // columns per tile, a multiple of 32
   int stages;         // of the ring
-  int m_blocks, num_tiles, k_tiles;
+  int inner;          // blocks of tokens: they change fastest, so that the CTAs in flight share W's tiles in L2
+  int num_tiles, k_tiles;
   int* st;
   uint64_t wait_ns;
   int hold;
@@ -85,7 +87,9 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, WaitStat
   return __all_sync(0xFFFFFFFFu, mbar_wait_inline<CG == 2>(bar, parity, w, st)) != 0;
 }
 
-template <int CG, bool BF16OUT>
+// SWAP: the tiles' rows are channels (W is the tensor cores' A) and their columns
+// tokens, for token counts that fill tiles better along the columns' finer grid.
+template <int CG, bool BF16OUT, bool SWAP>
 __global__ void __launch_bounds__(THREADS, 1)
     k_i8_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t ph = 0;
     bool ok = !p.hold;
     for (int tile = group; ok && tile < p.num_tiles; tile += groups) {
-      const int mb = tile % p.m_blocks, nb = tile / p.m_blocks;
+      const int mb = SWAP ? tile / p.inner : tile % p.inner, nb = SWAP ? tile % p.inner : tile / p.inner;
       const int a_row = (mb * CG + (int)rank) * BM, w_row = nb * p.bn + (int)rank * (p.bn / CG);
       for (int kt = 0; kt < p.k_tiles; ++kt) {
         ok = wait_all<CG>(saddr(&empty[s]), ph ^ 1u, ws, p.st);
@@ -217,15 +221,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t quad = (uint32_t)(q * 32) << 16;
     int local = 0;
     for (int tile = group; tile < p.num_tiles; tile += groups, ++local) {
-      const int mb = tile % p.m_blocks, nb = tile / p.m_blocks, b = local & 1;
+      const int mb = SWAP ? tile / p.inner : tile % p.inner, nb = SWAP ? tile % p.inner : tile / p.inner, b = local & 1;
       const int row0 = (mb * CG + (int)rank) * BM + q * 32, n0 = nb * p.bn, n_end = min(p.N, n0 + p.bn);
       float* ct = cols + b * 2 * BN_MAX;
       for (int c = et; c < p.bn; c += 32 * EPI_WARPS) {
         const bool in = n0 + c < p.N;
-        ct[c] = in ? p.w_scales[n0 + c] : 0.0f;
-        ct[BN_MAX + c] = in && p.bias != nullptr ? p.bias[n0 + c] : 0.0f;
+        ct[c] = in ? (SWAP ? p.a_scales : p.w_scales)[n0 + c] : 0.0f;
+        ct[BN_MAX + c] = !SWAP && in && p.bias != nullptr ? p.bias[n0 + c] : 0.0f;
       }
-      const float sa = row0 + lane < p.M ? p.a_scales[row0 + lane] : 0.0f;
+      const bool row_in = row0 + lane < p.M;
+      const float sr = row_in ? (SWAP ? p.w_scales : p.a_scales)[row0 + lane] : 0.0f;
+      const float bias_r = SWAP && row_in && p.bias != nullptr ? p.bias[row0 + lane] : 0.0f;
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (!warp_wait<CG == 2>(saddr(&acc_full[b]), (uint32_t)((local >> 1) & 1), ws, p.st)) break;
       tc_fence_after();
@@ -246,16 +252,36 @@ __global__ void __launch_bounds__(THREADS, 1)
         else tmem_ld16(tmem + quad + (uint32_t)(b * BN_MAX + c0), r);
         tmem_ld_wait();
         if (c0 + 2 * W >= c_end) release();
+        if constexpr (SWAP) {
+          // a lane's row is a column of Y: one token's 32 columns a store
+          using Out = std::conditional_t<BF16OUT, __nv_bfloat16, float>;
+          Out* y = static_cast<Out*>(p.y) + (int64_t)(n0 + c0) * p.ldy + row0 + lane;
+          const int left = row_in ? n_end - n0 - c0 : 0;
+#pragma unroll
+          for (int i = 0; i < W; i += 4) {
+            const float4 t = *reinterpret_cast<const float4*>(ct + c0 + i);
+            const float s4[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e, y += p.ldy) {
+              const float f = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn((int)r[i + e]), s4[e]), sr), bias_r);
+              if (i + e < left) {
+                if constexpr (BF16OUT) *y = __float2bfloat16_rn(f);
+                else *y = f;
+              }
+            }
+          }
+          continue;
+        }
         const float4* sw4 = reinterpret_cast<const float4*>(ct + c0);
         const float4* bi4 = reinterpret_cast<const float4*>(ct + BN_MAX + c0);
         float v[W];
 #pragma unroll
         for (int i = 0; i < W / 4; ++i) {
           const float4 s4 = sw4[i], b4 = bi4[i];
-          v[4 * i] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * i]), sa), s4.x), b4.x);
-          v[4 * i + 1] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * i + 1]), sa), s4.y), b4.y);
-          v[4 * i + 2] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * i + 2]), sa), s4.z), b4.z);
-          v[4 * i + 3] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * i + 3]), sa), s4.w), b4.w);
+          v[4 * i] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * i]), sr), s4.x), b4.x);
+          v[4 * i + 1] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * i + 1]), sr), s4.y), b4.y);
+          v[4 * i + 2] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * i + 2]), sr), s4.z), b4.z);
+          v[4 * i + 3] = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn((int)r[4 * i + 3]), sr), s4.w), b4.w);
         }
         uint4* mine = reinterpret_cast<uint4*>(buf + lane * EPI_PITCH);
 #pragma unroll
@@ -311,26 +337,27 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-template <int CG>
+template <int CG, bool SWAP>
 cudaError_t launch_tiles(const I8GemmArgs& g, int bn, int num_sms, cudaStream_t stream) {
-  const int64_t mb = (g.M + BM * CG - 1) / (BM * CG), nb = (g.N + bn - 1) / bn;
+  const int64_t rows = SWAP ? g.N : g.M, columns = SWAP ? g.M : g.N;
+  const int64_t mb = (rows + BM * CG - 1) / (BM * CG), nb = (columns + bn - 1) / bn;
   if (mb * nb > INT32_MAX - 4096) return cudaErrorNotSupported;    // 32-bit tile numbers, one grid beyond the last
-  CUtensorMap tmA, tmB;
-  if (!encode_i8_map(&tmA, g.a, g.M, g.K, g.lda, BM) ||
-      !encode_i8_map(&tmB, g.w, g.N, g.K, g.ldw, (uint32_t)(bn / CG)))
+  CUtensorMap tmA, tmW;
+  if (!encode_i8_map(&tmA, g.a, g.M, g.K, g.lda, (uint32_t)(SWAP ? bn / CG : BM)) ||
+      !encode_i8_map(&tmW, g.w, g.N, g.K, g.ldw, (uint32_t)(SWAP ? BM : bn / CG)))
     return cudaErrorInvalidValue;
   Params p{};
   p.a_scales = g.a_scales; p.w_scales = g.w_scales; p.bias = g.bias;
   p.y = g.y; p.ldy = g.ldy;
   const size_t esize = g.y_bf16 ? 2 : 4;
   p.y_vec = reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && ((size_t)g.ldy * esize) % 16 == 0;
-  p.M = (int)g.M; p.N = (int)g.N; p.K = (int)g.K; p.bn = bn;
+  p.M = (int)rows; p.N = (int)columns; p.K = (int)g.K; p.bn = bn;
   p.stages = std::min(MAX_STAGES, RING_BYTES / stage_bytes(CG, bn));
-  p.m_blocks = (int)mb; p.num_tiles = (int)(mb * nb); p.k_tiles = (int)((g.K + BK - 1) / BK);
+  p.inner = (int)(SWAP ? nb : mb); p.num_tiles = (int)(mb * nb); p.k_tiles = (int)((g.K + BK - 1) / BK);
   p.st = g.st;
   const WaitTest wt = wait_test();
   p.wait_ns = wt.limit_ns; p.hold = wt.hold;
-  auto kern = g.y_bf16 ? k_i8_gemm<CG, true> : k_i8_gemm<CG, false>;
+  auto kern = g.y_bf16 ? k_i8_gemm<CG, true, SWAP> : k_i8_gemm<CG, false, SWAP>;
   static SmemOnce once[2];
   cudaError_t e = once[g.y_bf16 ? 1 : 0].set(kern, SMEM_BYTES);
   if (e != cudaSuccess) return e;
@@ -346,7 +373,7 @@ cudaError_t launch_tiles(const I8GemmArgs& g, int bn, int num_sms, cudaStream_t 
   at[1].val.clusterDim.x = CG; at[1].val.clusterDim.y = 1; at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = CG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, tmA, tmB, p);
+  return cudaLaunchKernelEx(&cfg, kern, SWAP ? tmW : tmA, SWAP ? tmA : tmW, p);
 }
 
 }  // namespace
@@ -373,21 +400,27 @@ cudaError_t launch_i8_gemm(const I8GemmArgs& g, int num_sms, cudaStream_t stream
   // Up to 128 tokens W's rows fill the tensor cores' M better than the tokens do
   // (128 x 5120 x 5120: 11.6 us, tiles of 256 tokens x 96 columns 13.8).
   if (g.M <= 128) return launch_i8_gemm_few(g, num_sms, stream);
-  // Beyond, tiles of 256 tokens by a pair of CTAs; their width by an estimate: a
-  // K-slice takes 84 ns + 1 ns a column, and 222 ns at least (measured, 128 to 256
-  // columns); filling, the last epilogue and the launch come on top.  Up to 256
+  // Beyond, tiles of a pair of CTAs, 256 tokens x bn channels or 256 channels x bn
+  // tokens, by an estimate: a K-slice takes 84 ns + 1 ns a column, and 222 ns at
+  // least (measured, 128 to 256 columns); filling, the last epilogue and the launch
+  // come on top (777 x 11008 x 4096: 160 tokens wide 32.4 us, 224 channels wide
+  // 35.6; 512 x 4096 x 14336: 128 channels wide 29.4, 224 wide 33.0).  Up to 256
   // tokens splitting K instead can win (256 x 5120 x 27648: 40 us, tiles 52 us;
   // 256 x 4096 x 4096: 13.7 and 11.5 us).
-  const int64_t k_tiles = (g.K + BK - 1) / BK, mb = (g.M + 2 * BM - 1) / (2 * BM), pairs = std::max(1, num_sms / 2);
+  const int64_t k_tiles = (g.K + BK - 1) / BK, pairs = std::max(1, num_sms / 2);
   double best = 0.0;
   int bn = 0;
-  for (int c = 32; c <= BN_MAX; c += 32) {
-    const int64_t waves = (mb * ((g.N + c - 1) / c) + pairs - 1) / pairs;
-    const double ns = 5000.0 + 8.0 * c + (double)(waves * k_tiles) * std::max(222.0, 84.0 + c);
-    if (bn == 0 || ns <= best) { best = ns; bn = c; }
+  bool swap = false;
+  for (int side = 0; side < 2; ++side) {
+    const int64_t rows = side ? g.N : g.M, columns = side ? g.M : g.N, mb = (rows + 2 * BM - 1) / (2 * BM);
+    for (int c = 32; c <= BN_MAX; c += 32) {
+      const int64_t waves = (mb * ((columns + c - 1) / c) + pairs - 1) / pairs;
+      const double ns = 5000.0 + 8.0 * c + (double)(waves * k_tiles) * std::max(222.0, 84.0 + c) + (side ? 500.0 : 0.0);
+      if (bn == 0 || ns < best || (!side && ns <= best)) { best = ns; bn = c; swap = side != 0; }
+    }
   }
   if (g.M <= 256 && i8_gemm_few_ns(g.M, g.N, g.K, num_sms) < best) return launch_i8_gemm_few(g, num_sms, stream);
-  return launch_tiles<2>(g, bn, num_sms, stream);
+  return swap ? launch_tiles<2, true>(g, bn, num_sms, stream) : launch_tiles<2, false>(g, bn, num_sms, stream);
 }
 
 }  // namespace nvfp4
