@@ -55,7 +55,7 @@ struct Params {
   const float* bias;
   void* y;
   int64_t ldy;
-  int y_vec;          // Y's base and row pitch allow 16-byte stores
+  int y_align;        // bytes that Y's base and row pitch are multiples of: 16, 4 or 2
   int M, N, K;        // of the tiles: SWAP has the channels as M and the tokens as N
   int bn;             // columns per tile, a multiple of 32
   int stages;         // of the ring
@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - 4) >> 2, et = threadIdx.x - 128;
+    using Out = std::conditional_t<BF16OUT, __nv_bfloat16, float>;
     constexpr int W = BF16OUT ? 32 : 16;                 // columns staged at a time: rows of 64 bytes
     constexpr int PER = BF16OUT ? 8 : 4;                 // elements per 16-byte segment
     uint32_t* buf = epi + (warp - 4) * 32 * EPI_PITCH;
@@ -254,7 +255,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (c0 + 2 * W >= c_end) release();
         if constexpr (SWAP) {
           // a lane's row is a column of Y: one token's 32 columns a store
-          using Out = std::conditional_t<BF16OUT, __nv_bfloat16, float>;
           Out* y = static_cast<Out*>(p.y) + (int64_t)(n0 + c0) * p.ldy + row0 + lane;
           const int left = row_in ? n_end - n0 - c0 : 0;
 #pragma unroll
@@ -294,27 +294,41 @@ __global__ void __launch_bounds__(THREADS, 1)
                                  __float_as_uint(v[4 * g + 2]), __float_as_uint(v[4 * g + 3]));
         }
         __syncwarp();
-        // four lanes per row segment of 64 bytes, eight rows a store
-        const int col = n0 + c0 + (lane & 3) * PER, left = n_end - col;
+        if (p.y_align == 16) {
+          // four lanes per row segment of 64 bytes, eight rows a store
+          const int col = n0 + c0 + (lane & 3) * PER, left = n_end - col;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int lr = h * 8 + (lane >> 2), row = row0 + lr;
-          const uint32_t* src = buf + lr * EPI_PITCH + (lane & 3) * 4;
-          if (row < p.M && left > 0) {
-            const int64_t off = (int64_t)row * p.ldy + col;
-            if (p.y_vec && left >= PER) {
-              const uint4 o = *reinterpret_cast<const uint4*>(src);
-              if (BF16OUT) *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.y) + off) = o;
-              else *reinterpret_cast<uint4*>(reinterpret_cast<float*>(p.y) + off) = o;
-            } else {
-              for (int e = 0; e < PER && e < left; ++e) {
-                if (BF16OUT)
-                  reinterpret_cast<__nv_bfloat16*>(p.y)[off + e] = reinterpret_cast<const __nv_bfloat16*>(src)[e];
-                else
-                  reinterpret_cast<float*>(p.y)[off + e] = reinterpret_cast<const float*>(src)[e];
+          for (int h = 0; h < 4; ++h) {
+            const int lr = h * 8 + (lane >> 2), row = row0 + lr;
+            const uint32_t* src = buf + lr * EPI_PITCH + (lane & 3) * 4;
+            if (row < p.M && left > 0) {
+              const int64_t off = (int64_t)row * p.ldy + col;
+              if (left >= PER) {
+                *reinterpret_cast<uint4*>(static_cast<Out*>(p.y) + off) = *reinterpret_cast<const uint4*>(src);
+              } else {
+                for (int e = 0; e < left; ++e) static_cast<Out*>(p.y)[off + e] = reinterpret_cast<const Out*>(src)[e];
               }
             }
           }
+        } else if (!BF16OUT || p.y_align == 4) {
+          // sixteen lanes per row segment, a word each (odd row pitches of fp32, even ones of bf16)
+          constexpr int EW = BF16OUT ? 2 : 1;
+          const int col = n0 + c0 + (lane & 15) * EW, left = n_end - col;
+          Out* y = static_cast<Out*>(p.y) + (int64_t)(row0 + (lane >> 4)) * p.ldy + col;
+          const uint32_t* src = buf + (lane >> 4) * EPI_PITCH + (lane & 15);
+          for (int row = row0 + (lane >> 4), h = 0; h < 16; ++h, row += 2, y += 2 * p.ldy, src += 2 * EPI_PITCH) {
+            if (row >= p.M || left <= 0) continue;
+            if (left >= EW) *reinterpret_cast<uint32_t*>(y) = *src;
+            else *y = *reinterpret_cast<const Out*>(src);
+          }
+        } else {
+          // odd row pitches of bf16: a whole warp per row segment (8 elements a lane took 1014 us for 6978 x 23122 x 3472)
+          const int col = n0 + c0 + lane;
+          Out* y = static_cast<Out*>(p.y) + (int64_t)row0 * p.ldy + col;
+          const Out* src = reinterpret_cast<const Out*>(buf) + lane;
+          const int rows = col < n_end ? min(32, p.M - row0) : 0;
+#pragma unroll 4
+          for (int h = 0; h < rows; ++h, y += p.ldy, src += 2 * EPI_PITCH) *y = *src;
         }
         __syncwarp();
       }
@@ -349,8 +363,8 @@ cudaError_t launch_tiles(const I8GemmArgs& g, int bn, int num_sms, cudaStream_t 
   Params p{};
   p.a_scales = g.a_scales; p.w_scales = g.w_scales; p.bias = g.bias;
   p.y = g.y; p.ldy = g.ldy;
-  const size_t esize = g.y_bf16 ? 2 : 4;
-  p.y_vec = reinterpret_cast<uintptr_t>(g.y) % 16 == 0 && ((size_t)g.ldy * esize) % 16 == 0;
+  const uint64_t bytes = reinterpret_cast<uintptr_t>(g.y) | ((uint64_t)g.ldy * (g.y_bf16 ? 2 : 4));
+  p.y_align = bytes % 16 == 0 ? 16 : bytes % 4 == 0 ? 4 : 2;
   p.M = (int)rows; p.N = (int)columns; p.K = (int)g.K; p.bn = bn;
   p.stages = std::min(MAX_STAGES, RING_BYTES / stage_bytes(CG, bn));
   p.inner = (int)(SWAP ? nb : mb); p.num_tiles = (int)(mb * nb); p.k_tiles = (int)((g.K + BK - 1) / BK);
