@@ -404,8 +404,8 @@ nvfp4_status nvfp4_i8_gemm(const int8_t* a_codes, int64_t lda, const float* a_sc
 /* Test support for the device-side bounded waits (failure detection around
  * the method; the pages have no counterpart).  Every mbarrier wait of the
  * tensor-core kernels (nvfp4_gemm, nvfp4_gemm_residue, the fused decode
- * linears, the MXFP4 GEMMs) gives up after limit_ns nanoseconds (default 4 s;
- * 0 restores it), records NVFP4_ERR_TIMEOUT in *dev_status and lets the launch
+ * linears, the MXFP4 GEMMs, nvfp4_i8_gemm beyond four rows) gives up after
+ * limit_ns nanoseconds (default 4 s; 0 restores it), records NVFP4_ERR_TIMEOUT in *dev_status and lets the launch
  * finish: each CTA first lets its own bulk copies and MMAs in flight and the
  * bytes its cluster peers send complete, then releases its tensor memory and
  * exits, so the context stays usable.  withhold != 0 makes those kernels skip
