@@ -700,6 +700,123 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_ln_backward_rows(const BwdAr
   }
 }
 
+// Small inputs, in one launch: dgamma and dbeta need no sums over a row, so the
+// first CTAs take rows, for dx, and the rest take columns, for the parameters'
+// gradients, reading x and dy a second time (from L2).  A column CTA takes 32
+// bytes of every row: a warp four rows at a time, eight lanes of a word each; its
+// warps' sums are joined in shared memory in their order.  Bound: latency (333 x
+// 5120 bf16: 7.6 us; its bytes, once, 1.6).
+constexpr int kSmallThreads = 512;
+
+template <typename T, typename P, int V>
+__global__ void __launch_bounds__(kSmallThreads, 2) k_ln_backward_small(const BwdArgs a, int warps, int row_ctas, float* dgamma,
+                                                                         float* dbeta) {
+  using U = Unit<T>;
+  constexpr int C = 4 / (int)sizeof(T);               // columns per lane
+  __shared__ float2 red[kSmallThreads / 32];
+  __shared__ float sums[2][kSmallThreads / 32][8 * C];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  tc::griddep_launch_dependents();
+  tc::griddep_wait();
+  if ((int)blockIdx.x < row_ctas) {
+    const int index = w / warps, base = index * warps, span = warps * 32, t = (w - base) * 32 + lane;
+    const int64_t row = (int64_t)blockIdx.x * (kSmallThreads / 32 / warps) + index;
+    if (index >= kSmallThreads / 32 / warps || row >= a.M) return;     // whole teams
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float xh[V][8], g[V][8];
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int u = i * span + t;
+      if (u >= a.units) continue;
+      U p, q;
+      p.load(x, u, a.units);
+      q.load(dy, u, a.units);
+      float gm[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+      if (a.gamma != nullptr) U::param(static_cast<const P*>(a.gamma), u, a.units, gm);
+      p.unpack(xh[i]);
+      q.unpack(g[i]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        xh[i][e] = (xh[i][e] - mean) * rstd;
+        g[i][e] *= gm[e];
+        s.x += g[i][e];
+        s.y = fmaf(g[i][e], xh[i][e], s.y);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, o);
+      s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, o);
+    }
+    if (warps > 1) {
+      if (lane == 0) red[w] = s;
+      asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(span) : "memory");
+      s = red[base];
+      for (int k = 1; k < warps; ++k) {
+        s.x += red[base + k].x;
+        s.y += red[base + k].y;
+      }
+    }
+    const float inv_k = 1.0f / (8.0f * (float)a.units), c1 = s.x * inv_k, c2 = s.y * inv_k;
+    T* dx = static_cast<T*>(a.dx) + row * a.lddx;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int u = i * span + t;
+      if (u >= a.units) continue;
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = rstd * (g[i][e] - fmaf(xh[i][e], c2, c1));
+      U::store(dx, u, a.units, o);
+    }
+    return;
+  }
+  const int col = ((int)blockIdx.x - row_ctas) * 8 * C + (lane & 7) * C;   // K is a multiple of 8 * C
+  float sg[C] = {}, sb[C] = {};
+#pragma unroll 4
+  for (int64_t row = w * 4 + (lane >> 3); row < a.M; row += kSmallThreads / 8) {
+    const uint32_t xw = *reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.x) + row * a.ldx + col);
+    const uint32_t dw = *reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.dy) + row * a.lddy + col);
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float xv[C], dv[C];
+    if constexpr (C == 2) {
+      xv[0] = __uint_as_float(xw << 16); xv[1] = __uint_as_float(xw & 0xFFFF0000u);
+      dv[0] = __uint_as_float(dw << 16); dv[1] = __uint_as_float(dw & 0xFFFF0000u);
+    } else {
+      xv[0] = __uint_as_float(xw);
+      dv[0] = __uint_as_float(dw);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      sg[c] = fmaf(dv[c], (xv[c] - mean) * rstd, sg[c]);
+      sb[c] += dv[c];
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+      sg[c] += __shfl_xor_sync(0xFFFFFFFFu, sg[c], o);
+      sb[c] += __shfl_xor_sync(0xFFFFFFFFu, sb[c], o);
+    }
+    if (lane < 8) {
+      sums[0][w][lane * C + c] = sg[c];
+      sums[1][w][lane * C + c] = sb[c];
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < 16 * C) {
+    const int which = threadIdx.x / (8 * C), c = threadIdx.x % (8 * C);
+    float v = sums[which][0][c];
+#pragma unroll
+    for (int k = 1; k < kSmallThreads / 32; ++k) v += sums[which][k][c];
+    float* out = which == 0 ? dgamma : dbeta;
+    if (out != nullptr) out[((int)blockIdx.x - row_ctas) * 8 * C + c] = v;
+  }
+}
+
 // Rows too long for that ring.
 // The rows' units beyond blockDim.x * V are taken in further column chunks
 // (blockIdx.y), each of which forms the row sums over the whole row again.
@@ -823,17 +940,26 @@ cudaError_t run_backward_rows(const BwdArgs& a, int warps, int teams, int stages
   return cudaLaunchKernelEx(&cfg, k_ln_backward_rows<T, P, V>, a, warps, stages);
 }
 
+template <typename T, typename P>
+cudaError_t run_backward_small(const BwdArgs& a, float* dgamma, float* dbeta, cudaStream_t stream) {
+  const int v = a.units > kSmallThreads / 2 ? 2 : 1;         // units per thread
+  const int warps = (a.units + 32 * v - 1) / (32 * v), teams = kSmallThreads / 32 / warps;
+  const int row_ctas = a.dx != nullptr ? (int)((a.M + teams - 1) / teams) : 0;
+  const int col_ctas = dgamma != nullptr || dbeta != nullptr ? a.units * (int)sizeof(T) / 4 : 0;
+  cudaLaunchAttribute at;
+  const cudaLaunchConfig_t cfg = dependent_launch(dim3((unsigned)(row_ctas + col_ctas)), kSmallThreads, 0, stream, &at);
+  return cudaLaunchKernelEx(&cfg, v == 2 ? k_ln_backward_small<T, P, 2> : k_ln_backward_small<T, P, 1>, a, warps, row_ctas,
+                            dgamma, dbeta);
+}
+
 // *parts: rows of the workspace that were written.
 template <typename T, typename P>
 cudaError_t run_backward(const BwdArgs& a, int num_sms, int* parts, cudaStream_t stream) {
   const int most = std::min(num_sms, kLnMaxParts);
-  // Units per thread: few rows, more threads on each (64 x 4096 bf16: one 7.1 us,
-  // two 8.1, four 10.1; 333 x 5120: two 12.2, four 12.6); many, more rows at a time
-  // (8192 x 8192 bf16: four 88 us, two 106), unless a row is short (1024: four 23
-  // us, two 19).  Halved until a team's rows fit in shared memory twice.
-  int v = a.M <= num_sms ? 1 : a.M <= 4 * (int64_t)num_sms || a.units < 256 ? 2 : 4;
-  while (v < 4 && (a.units + 32 * v - 1) / (32 * v) > kBwdThreads / 32) v *= 2;
-  for (; v >= 1; v /= 2) {
+  // Units per thread: four, for more rows at a time (8192 x 8192 bf16: four 88 us,
+  // two 106), but two for short rows (8192 x 1024: 19 us, four 23) and where four
+  // leave a team no room for two rows in shared memory (8192 x 8192 fp32).
+  for (int v = a.units < 256 ? 2 : 4; v >= 2; v /= 2) {
     const int warps = (a.units + 32 * v - 1) / (32 * v);
     if (warps > kBwdThreads / 32) break;
     const int teams = std::min(kBwdThreads / 32 / warps, 15);
@@ -842,8 +968,7 @@ cudaError_t run_backward(const BwdArgs& a, int num_sms, int* parts, cudaStream_t
     if (stages < 2) continue;
     *parts = (int)std::min<int64_t>(most, (a.M + teams - 1) / teams);
     if (v == 4) return run_backward_rows<T, P, 4>(a, warps, teams, stages, *parts, stream);
-    if (v == 2) return run_backward_rows<T, P, 2>(a, warps, teams, stages, *parts, stream);
-    return run_backward_rows<T, P, 1>(a, warps, teams, stages, *parts, stream);
+    return run_backward_rows<T, P, 2>(a, warps, teams, stages, *parts, stream);
   }
   const int threads = std::min(512, (a.units + 63) / 64 * 32);
   *parts = (int)std::min<int64_t>(most, a.M);
@@ -882,6 +1007,17 @@ cudaError_t launch_layernorm_backward(const LayerNormBwdArgs& n, int num_sms, cu
   const bool params = n.dgamma != nullptr || n.dbeta != nullptr;
   a.part = params ? n.part : nullptr;
   a.M = n.M; a.units = (int)(n.K / 8);
+  // k_ln_backward_small while reading x and dy twice costs less than the second
+  // launch and the partial sums: 333 x 5120 bf16 7.6 us, the two kernels 12.6; 64 x
+  // 4096 3.2 and 7.3; 1000 x 8192 (33 MB) 21 and 27; 2000 x 2048 14.0 and 15.6; but
+  // 4000 x 256 10.4 and 8.4, 1500 x 5120 fp32 (61 MB) 37 and 26.
+  if (n.M <= 2048 && 2 * n.M * n.K * (n.dt == NVFP4_BF16 ? 2 : 4) <= (36ll << 20) && a.units <= 2 * kSmallThreads) {
+    if (n.dt == NVFP4_BF16)
+      return n.pdt == NVFP4_BF16 ? run_backward_small<__nv_bfloat16, __nv_bfloat16>(a, n.dgamma, n.dbeta, stream)
+                                 : run_backward_small<__nv_bfloat16, float>(a, n.dgamma, n.dbeta, stream);
+    return n.pdt == NVFP4_BF16 ? run_backward_small<float, __nv_bfloat16>(a, n.dgamma, n.dbeta, stream)
+                               : run_backward_small<float, float>(a, n.dgamma, n.dbeta, stream);
+  }
   int parts = 0;
   cudaError_t e;
   if (n.dt == NVFP4_BF16)

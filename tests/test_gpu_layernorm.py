@@ -125,8 +125,9 @@ def test_layernorm_without_parameters(with_gamma, with_beta):
     assert torch.equal(y.cpu(), torch.from_numpy(ry).to(BF))
 
 
-def test_layernorm_in_place():
-    x, xn = inputs(65, 8192, F32, 5)
+@pytest.mark.parametrize("rows", [65, 700])
+def test_layernorm_in_place(rows):
+    x, xn = inputs(rows, 8192, F32, 5)
     ry, _, _ = layernorm(xn)
     nv.nvfp4_layernorm(x, x)
     assert torch.equal(x.cpu(), torch.from_numpy(ry))
@@ -164,7 +165,8 @@ def test_layernorm_nonfinite_rows():
     assert st.item() == 5 and torch.isnan(y[:2, :64]).all()
 
 
-BWD = [(1, 16), (2, 48), (5, 256), (333, 1024), (149, 8208), (700, 4096), (4, 14336), (2, 33040), (1000, 80)]
+BWD = [(1, 16), (2, 48), (5, 256), (333, 1024), (149, 8208), (700, 4096), (4, 14336), (2, 33040), (1000, 80), (3, 8192),
+       (2100, 272), (2500, 1024), (1300, 8192), (600, 10256), (2049, 64), (500, 16384)]
 
 
 @pytest.mark.parametrize("rows,cols", BWD)
@@ -199,16 +201,17 @@ def test_layernorm_backward(rows, cols, dtype, pdt):
     assert (np.abs(db.double().cpu().numpy() - rb) <= deep_col * HALF * mb + 1e-38).all()
 
 
-def test_layernorm_backward_parts():
+@pytest.mark.parametrize("rows", [300, 2300])
+def test_layernorm_backward_parts(rows):
     """Any of the three gradients alone is the one of the full call; without a gain it is one."""
-    x, xn = inputs(300, 512, F32, 2)
-    dy = torch.randn(300, 512, device="cuda")
+    x, xn = inputs(rows, 512, F32, 2)
+    dy = torch.randn(rows, 512, device="cuda")
     _, mean, rstd = layernorm(xn)
     m, r = torch.from_numpy(mean).cuda(), torch.from_numpy(rstd).cuda()
-    ws = nv.LayerNormWorkspace(300, 512)
+    ws = nv.LayerNormWorkspace(rows, 512)
 
     def grads(gamma, want):
-        t = [torch.empty(300, 512, device="cuda"), torch.empty(512, device="cuda"), torch.empty(512, device="cuda")]
+        t = [torch.empty(rows, 512, device="cuda"), torch.empty(512, device="cuda"), torch.empty(512, device="cuda")]
         a = [v if w else None for v, w in zip(t, want)]
         nv.nvfp4_layernorm_backward(dy, x, m, r, a[0], gamma, a[1], a[2], ws if want[1] or want[2] else None)
         return a
