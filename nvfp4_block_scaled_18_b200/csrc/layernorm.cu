@@ -18,7 +18,8 @@ namespace nvfp4 {
 using namespace rows;
 namespace {
 
-constexpr int MAXT(int v) { return v <= 2 ? 1024 : v == 4 ? 640 : 512; }    // threads of a CTA, by registers per thread
+// Threads of a CTA at most, by the registers that v units per thread take.
+constexpr int max_threads(int v) { return v <= 2 ? 1024 : v == 4 ? 640 : 512; }
 
 struct RowArgs {
   const void* x; int64_t ldx;
@@ -47,7 +48,7 @@ struct RowArgs {
 // kept: two rows per team (41 us), and sums in fp32, whose codes would depend on
 // the order.
 template <typename T, typename P, bool NORM, bool QUANT, int V, bool ONE, bool FULL>
-__global__ void __launch_bounds__(ONE ? MAXT(V) : 1024) k_rows(const RowArgs a) {
+__global__ void __launch_bounds__(ONE ? max_threads(V) : 1024) k_rows(const RowArgs a) {
   using Raw = Unit<T>;
   __shared__ double red_sum[2][kMaxWarps];
   __shared__ uint32_t red_max[2][kMaxWarps];
@@ -216,6 +217,7 @@ __device__ __forceinline__ void copies_left() { asm volatile("cp.async.wait_grou
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+
 // Layer norm of many long rows: the steps of k_rows with fewer warps per row (two
 // for 4096 elements), since a row's reductions cost every one of its warps some
 // hundred instructions and a barrier.  A thread holds V units as they are in
@@ -452,7 +454,7 @@ cudaError_t launch_norm_rows(const RowArgs& a, int num_sms, cudaStream_t stream)
 template <typename T, typename P, bool NORM, bool QUANT>
 cudaError_t launch_rows(const RowArgs& a, int num_sms, cudaStream_t stream) {
   constexpr bool BF16 = sizeof(T) == 2;
-  auto fits = [&](int v) { return a.units <= MAXT(v) * v; };
+  auto fits = [&](int v) { return a.units <= max_threads(v) * v; };
   // k_norm_rows: from 16 KB a row on (4800 x 8192 bf16: 39 us, k_rows 44; into 8 bits
   // 44 and 50; 4800 x 4096 bf16: 22.8 and 19.5), and where k_rows would read fp32
   // parameters beside bf16 rows, two lines a load (8192 x 4096: 31 and 37 us).
@@ -529,7 +531,7 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2* slot) {
 // spent on what is on its way), reads them once for the row's sums and the
 // parameters' gradients and once more for dx.  gamma waits in shared memory too:
 // from L1, which the ring leaves too small for it, 8192 x 8192 fp32 took 227 us.
-// Bound: bytes (8192 x 8192 fp32: 127 us, 6.35 TB/s; bf16: 88 us, where half the
+// Bound: bytes (8192 x 8192 fp32: 129 us, 6.25 TB/s; bf16: 95 us, where half the
 // bytes go with as many instructions).
 constexpr int kBwdThreads = 512, kBwdSmem = 224 * 1024, kBwdMaxStages = 4;
 

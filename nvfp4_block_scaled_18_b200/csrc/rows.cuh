@@ -7,7 +7,6 @@
 namespace nvfp4 {
 namespace rows {
 
-
 constexpr int kMaxWarps = 32;   // warps of one CTA
 
 // A team of warps.  `slot` is its area for one reduction (one word per warp); the
