@@ -20,6 +20,11 @@
 //              in segments of 16 bytes.  Two accumulators alternate, so a tile's
 //              epilogue runs under the next tile's MMAs.
 // Every mbarrier wait is bounded, as in the other tensor-core kernels.
+//
+// Bound: the tensor cores, 3.5 POP/s in bursts and 3.15 under the power cap (8192 x
+// 28672 x 8192: 1080 and 1223 us); for a few waves of tiles the filling and the
+// last epilogue, some 6 us, and the last wave's idle pairs (777 x 11008 x 4096:
+// 31 us, 2.2 POP/s).
 #include <algorithm>
 #include <type_traits>
 

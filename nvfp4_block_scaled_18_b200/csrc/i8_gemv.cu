@@ -4,7 +4,8 @@
 // each row and of each token at a time and multiplies them with dp4a, so W is
 // streamed once with wide loads and the tokens come from L1.  When there are
 // too few rows to fill the SMs, the S warps of a group split K; the int32 sums
-// are joined in shared memory, exactly.  Bound: W's bytes.
+// are joined in shared memory, exactly.  Bound: W's bytes (1 x 14336 x 4096: 11.1 us,
+// 5.3 TB/s; 4 x 14336 x 4096: 11.9).
 //
 // Programmatic dependent launch: before griddepcontrol.wait a warp only asks L2
 // to prefetch its first W bytes.
