@@ -1,11 +1,12 @@
-// 8-bit integer linear for one to eight tokens on the CUDA cores, sm_100a.
+// 8-bit integer linear for one to four tokens on the CUDA cores, sm_100a.
 //
-// A warp takes four rows of W (four columns of Y): each lane reads 16 bytes of
-// each row and of each token at a time and multiplies them with dp4a, so W is
-// streamed once with wide loads and the tokens come from L1.  When there are
-// too few rows to fill the SMs, the S warps of a group split K; the int32 sums
-// are joined in shared memory, exactly.  Bound: W's bytes (1 x 14336 x 4096: 11.1 us,
-// 5.3 TB/s; 4 x 14336 x 4096: 11.9).
+// A warp takes four rows of W (columns of Y) for one token, eight for more: each
+// lane reads 16 bytes of each row and of each token at a time and multiplies them
+// with dp4a, so W is streamed once with wide loads and the tokens come from L1.
+// When there are too few rows to fill the SMs, the S warps of a group split K;
+// the int32 sums are joined in shared memory, exactly.  Bound: W's bytes (1 x
+// 14336 x 4096: 11.1 us, 5.3 TB/s; 4 x 14336 x 4096: 11.9, with four rows a warp
+// 17.4).
 //
 // Programmatic dependent launch: before griddepcontrol.wait a warp only asks L2
 // to prefetch its first W bytes.
@@ -28,7 +29,7 @@ struct Params {
   const float* bias;
   void* y; int64_t ldy;
   int M, N, K;
-  int split;                   // S: warps that share four rows, 1, 2, 4 or 8
+  int split;                   // S: warps that share their rows, 1, 2, 4 or 8
 };
 
 // W passes once: past L1
@@ -54,8 +55,8 @@ __global__ void __launch_bounds__(WARPS * 32) k_i8_gemv(const Params p) {
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = WARPS / p.split, part = warp % p.split;
-  const int64_t quad = (int64_t)blockIdx.x * groups + warp / p.split;
-  const int n0 = (int)(quad * ROWS);
+  const int64_t run = (int64_t)blockIdx.x * groups + warp / p.split;
+  const int n0 = (int)(run * ROWS);
   // this warp's share of K in units of 16 bytes, 32 to a step
   const int units = p.K / 16, steps = (units + 31) / 32;
   const int t0 = (int)((int64_t)part * steps / p.split), t1 = (int)((int64_t)(part + 1) * steps / p.split);
@@ -146,12 +147,12 @@ cudaError_t launch_mt(const I8GemmArgs& g, int num_sms, cudaStream_t stream) {
   p.a = g.a; p.lda = g.lda; p.a_scales = g.a_scales; p.w = g.w; p.ldw = g.ldw; p.w_scales = g.w_scales;
   p.bias = g.bias; p.y = g.y; p.ldy = g.ldy; p.M = (int)g.M; p.N = (int)g.N; p.K = (int)g.K;
   constexpr int ROWS = rows_per_warp<MT>();
-  const int64_t quads = (g.N + ROWS - 1) / ROWS, steps = (g.K / 16 + 31) / 32;
+  const int64_t runs = (g.N + ROWS - 1) / ROWS, steps = (g.K / 16 + 31) / 32;
   // split K until there are this many warps for every SM, each with two steps or more
   constexpr int want = MT == 1 ? 16 : 8;
   p.split = 1;
-  while (p.split < WARPS && quads * p.split < (int64_t)want * num_sms && steps >= 4 * p.split) p.split *= 2;
-  const int64_t grid = (quads * p.split + WARPS - 1) / WARPS;
+  while (p.split < WARPS && runs * p.split < (int64_t)want * num_sms && steps >= 4 * p.split) p.split *= 2;
+  const int64_t grid = (runs * p.split + WARPS - 1) / WARPS;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(WARPS * 32);
