@@ -453,14 +453,19 @@ def _device(where: str, *tensors: Optional[torch.Tensor]) -> int:
     return dev
 
 
-def _rows(t: torch.Tensor, M: int, K: int, dtype, where: str, name: str) -> int:
-    """Row stride of a 2-D row-major tensor of this shape and dtype."""
-    if t.dtype is not dtype or t.shape != (M, K):
-        raise ValueError(f"{where}: {name} must be a row-major {M} x {K} tensor of {dtype}")
+def _row_stride(t: torch.Tensor, M: int, K: int, where: str, name: str) -> int:
+    """Row stride of an M x K row-major tensor."""
     ld, step = t.stride()
     if step != 1 and K > 1:
         raise ValueError(f"{where}: {name} must be row-major")
     return ld if M > 1 else (K + 15) // 16 * 16      # one row: its stride is never used
+
+
+def _rows(t: torch.Tensor, M: int, K: int, dtype, where: str, name: str) -> int:
+    """Row stride of a row-major tensor that must have this shape and dtype."""
+    if t.dtype is not dtype or t.shape != (M, K):
+        raise ValueError(f"{where}: {name} must be a row-major {M} x {K} tensor of {dtype}")
+    return _row_stride(t, M, K, where, name)
 
 
 def _vector(t: Optional[torch.Tensor], n: int, dtype, where: str, name: str) -> Optional[int]:
@@ -505,7 +510,7 @@ def nvfp4_i8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor
     where = "nvfp4_i8_quantize"
     dt = _dtype_code(x)
     M, K = x.shape
-    ldx, ldc = _rows(x, M, K, x.dtype, where, "x"), _rows(codes, M, K, torch.int8, where, "codes")
+    ldx, ldc = _row_stride(x, M, K, where, "x"), _rows(codes, M, K, torch.int8, where, "codes")
     sp = _vector(scales, M, torch.float32, where, "scales")
     dev = _device(where, x, codes, scales, dev_status)
     _call(dev, stream, where, load_library().nvfp4_i8_quantize,
@@ -520,7 +525,7 @@ def nvfp4_layernorm(x: torch.Tensor, y: torch.Tensor, gamma: Optional[torch.Tens
     where = "nvfp4_layernorm"
     dt = _dtype_code(x)
     M, K = x.shape
-    ldx, ldy = _rows(x, M, K, x.dtype, where, "x"), _rows(y, M, K, x.dtype, where, "y")
+    ldx, ldy = _row_stride(x, M, K, where, "x"), _rows(y, M, K, x.dtype, where, "y")
     gp, bp, pdt = _params(gamma, beta, K, where)
     mp, rp = _vector(mean, M, torch.float32, where, "mean"), _vector(rstd, M, torch.float32, where, "rstd")
     dev = _device(where, x, y, gamma, beta, mean, rstd, dev_status)
@@ -535,7 +540,7 @@ def nvfp4_layernorm_i8_quantize(x: torch.Tensor, codes: torch.Tensor, scales: to
     where = "nvfp4_layernorm_i8_quantize"
     dt = _dtype_code(x)
     M, K = x.shape
-    ldx, ldc = _rows(x, M, K, x.dtype, where, "x"), _rows(codes, M, K, torch.int8, where, "codes")
+    ldx, ldc = _row_stride(x, M, K, where, "x"), _rows(codes, M, K, torch.int8, where, "codes")
     sp = _vector(scales, M, torch.float32, where, "scales")
     gp, bp, pdt = _params(gamma, beta, K, where)
     dev = _device(where, x, codes, scales, gamma, beta, dev_status)
@@ -567,7 +572,7 @@ def nvfp4_layernorm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tens
     where = "nvfp4_layernorm_backward"
     dt = _dtype_code(x)
     M, K = x.shape
-    ldx, lddy = _rows(x, M, K, x.dtype, where, "x"), _rows(dy, M, K, x.dtype, where, "dy")
+    ldx, lddy = _row_stride(x, M, K, where, "x"), _rows(dy, M, K, x.dtype, where, "dy")
     lddx = _rows(dx, M, K, x.dtype, where, "dx") if dx is not None else K
     gp, _, pdt = _params(gamma, None, K, where)
     mp, rp = _vector(mean, M, torch.float32, where, "mean"), _vector(rstd, M, torch.float32, where, "rstd")

@@ -146,6 +146,19 @@ def test_layernorm_far_from_zero(shift):
     np.testing.assert_array_equal(y.cpu().numpy(), ry)
 
 
+@pytest.mark.parametrize("scale,eps", [(1e20, 1e-5), (1e-20, 0.0), (1e-20, 1e-38), (1e15, 0.0)])
+@pytest.mark.parametrize("rows,cols", [(7, 512), (500, 4096)])
+def test_layernorm_far_scales(rows, cols, scale, eps):
+    """Variances far outside the range of usual ones: the same statistics and results."""
+    x = (torch.randn(rows, cols, generator=torch.Generator().manual_seed(7)) * scale).cuda()
+    y, mean, rstd = torch.empty_like(x), torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    nv.nvfp4_layernorm(x, y, eps=eps, mean=mean, rstd=rstd)
+    ry, rm, rr = layernorm(x.cpu().numpy(), eps=eps)
+    np.testing.assert_array_equal(mean.cpu().numpy(), rm)
+    np.testing.assert_array_equal(rstd.cpu().numpy(), rr)
+    np.testing.assert_array_equal(y.cpu().numpy(), ry)
+
+
 def test_layernorm_nonfinite_rows():
     x = torch.randn(6, 512, device="cuda")
     x[1, 7], x[3, 0], x[4, 511] = float("nan"), float("inf"), -float("inf")
