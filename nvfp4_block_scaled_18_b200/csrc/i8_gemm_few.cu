@@ -21,6 +21,7 @@
 // and the last; joining K's parts and writing Y takes 2 us (16 tokens) to 4 us (128)
 // more (61 x 5120 x 27648: 27.3 us, 5.3 TB/s over all; 16 x 14336 x 4096: 12.1 us).
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "i8_tc.cuh"
@@ -260,18 +261,54 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// The largest split of K whose clusters fit one wave (whole clusters in GPCs of
-// 16 SMs), whose partial sums fit and which leaves a CTA enough steps to pay for
-// joining them: above 32 tokens ten (128 x 4096 x 4096: 10.1 us split in 3,
-// 10.6 in 4).
-template <int NP, int CTAS>
+template <int NP, int CTAS, bool BF16OUT>
+cudaLaunchConfig_t few_config(unsigned grid, int ks, cudaStream_t stream, cudaLaunchAttribute (&at)[2]) {
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)ks; at[1].val.clusterDim.y = 1; at[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = Cfg<NP, CTAS>::SMEM;
+  cfg.stream = stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+// Clusters of ks CTAs, one per SM, that the device holds at once: asked once per
+// device and split, since the GPCs' sizes differ (148 SMs held 33 clusters of four,
+// 132 CTAs; 36 of them took two waves, 64 x 4500 x 28672 41 us, in three parts 26).
+template <int NP, bool BF16OUT>
+int clusters_at_once(int ks, int num_sms) {
+  static std::atomic<int> cache[16][9];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) dev = 16;
+  const int known = dev < 16 ? cache[dev][ks].load(std::memory_order_relaxed) : 0;
+  if (known > 0) return known;
+  static SmemOnce once;
+  cudaLaunchAttribute at[2];
+  const cudaLaunchConfig_t cfg = few_config<NP, 1, BF16OUT>((unsigned)(num_sms * 8 / ks * ks), ks, nullptr, at);
+  int n = 0;
+  if (once.set(k_i8_few<NP, 1, BF16OUT>, Cfg<NP, 1>::SMEM) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, k_i8_few<NP, 1, BF16OUT>, &cfg) != cudaSuccess || n <= 0)
+    n = std::max(1, num_sms / ks / 2);            // not known: a low guess, which only splits K less
+  if (dev < 16) cache[dev][ks].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// The largest split of K whose clusters fit one wave (16 x 4096 x 14336 in 32
+// clusters of eight 12.4 us, of four 13.7), whose partial sums fit and
+// which leaves a CTA enough steps to pay for joining them: above 32 tokens ten
+// (128 x 4096 x 4096: 10.1 us split in 3, 10.6 in 4).
+template <int NP, int CTAS, bool BF16OUT>
 int choose_ks(int64_t M, int64_t tiles, int k_steps, int num_sms) {
-  int ks = 1;
-  for (int k = 2; k <= 8; ++k)
-    if (tiles * k <= (int64_t)(num_sms / 16) * (16 * CTAS / k) * k && k * (NP > 32 ? 10 : 1) <= k_steps &&
-        Cfg<NP, CTAS>::fits((int)M, k))
-      ks = k;
-  return ks;
+  for (int k = 8; k >= 2; --k)
+    if (tiles * k <= (int64_t)num_sms * CTAS && k * (NP > 32 ? 10 : 1) <= k_steps && Cfg<NP, CTAS>::fits((int)M, k) &&
+        tiles * 10 <= (int64_t)clusters_at_once<NP, BF16OUT>(k, num_sms) * (CTAS == 2 ? 22 : 10))   // two per SM leave fewer SMs over
+      return k;
+  return 1;
 }
 
 template <int NP, int CTAS, bool BF16OUT>
@@ -279,7 +316,7 @@ cudaError_t launch_np(const I8GemmArgs& g, int num_sms, cudaStream_t stream) {
   using C = Cfg<NP, CTAS>;
   const int64_t tiles = (g.N + W_ROWS - 1) / W_ROWS;
   const int k_steps = (int)((g.K + BK - 1) / BK);
-  const int ks = choose_ks<NP, CTAS>(g.M, tiles, k_steps, num_sms);
+  const int ks = choose_ks<NP, CTAS, BF16OUT>(g.M, tiles, k_steps, num_sms);
   if (tiles * ks > INT32_MAX) return cudaErrorNotSupported;
   CUtensorMap tmW, tmX;
   if (!encode_i8_map(&tmW, g.w, g.N, g.K, g.ldw, W_ROWS) || !encode_i8_map(&tmX, g.a, g.M, g.K, g.lda, NP))
@@ -295,18 +332,8 @@ cudaError_t launch_np(const I8GemmArgs& g, int num_sms, cudaStream_t stream) {
   static SmemOnce once;
   cudaError_t e = once.set(kern, C::SMEM);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(tiles * ks));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = C::SMEM;
-  cfg.stream = stream;
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = (unsigned)ks; at[1].val.clusterDim.y = 1; at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 2;
+  const cudaLaunchConfig_t cfg = few_config<NP, CTAS, BF16OUT>((unsigned)(tiles * ks), ks, stream, at);
   return cudaLaunchKernelEx(&cfg, kern, tmW, tmX, p);
 }
 
@@ -335,7 +362,7 @@ cudaError_t launch_out(const I8GemmArgs& g, int num_sms, cudaStream_t stream) {
 
 double i8_gemm_few_ns(int64_t M, int64_t N, int64_t K, int num_sms) {
   const int64_t tiles = (N + W_ROWS - 1) / W_ROWS;
-  const int k_steps = (int)((K + BK - 1) / BK), ks = choose_ks<256, 1>(M, tiles, k_steps, num_sms);
+  const int k_steps = (int)((K + BK - 1) / BK), ks = choose_ks<256, 1, true>(M, tiles, k_steps, num_sms);
   const int64_t waves = (tiles * ks + num_sms - 1) / num_sms;
   return 10000.0 + 460.0 * (double)waves * (double)((k_steps + ks - 1) / ks);
 }
