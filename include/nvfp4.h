@@ -411,6 +411,8 @@ nvfp4_status nvfp4_i8_gemm(const int8_t* a_codes, int64_t lda, const float* a_sc
  * exits, so the context stays usable.  withhold != 0 makes those kernels skip
  * loading their weight tiles (the large-M GEMM: every operand tile), so that
  * their waits run out: a way to exercise the timeout path that faults nothing.
+ * withhold == 2: nvfp4_i8_gemm beyond 256 rows loads as usual, and one of the
+ * warps that write Y gives up at once in each CTA (the other kernels: as 1).
  * Output contents of a launch that timed out are unspecified.  The setting is
  * process wide, read when a launch is made, and meant for tests only. */
 void nvfp4_test_wait_fault(uint64_t limit_ns, int withhold);

@@ -117,12 +117,13 @@ def status_string(status: int) -> str:
         return STATUS_NAMES.get(status, "unknown")
 
 
-def nvfp4_test_wait_fault(limit_ns: int = 0, withhold: bool = False) -> None:
+def nvfp4_test_wait_fault(limit_ns: int = 0, withhold: int = 0) -> None:
     """Test support: bound every device-side wait of the tensor-core kernels by
     limit_ns (0 = the default 4 s); withhold=True makes the following launches
     skip their weight-tile loads so that the waits run out (NVFP4_ERR_TIMEOUT
-    in dev_status).  Process wide; for tests only."""
-    load_library().nvfp4_test_wait_fault(int(limit_ns), 1 if withhold else 0)
+    in dev_status); withhold=2 lets one output warp of each CTA of nvfp4_i8_gemm's
+    tile kernel give up instead.  Process wide; for tests only."""
+    load_library().nvfp4_test_wait_fault(int(limit_ns), int(withhold))
 
 
 def nvfp4_version() -> str:

@@ -175,7 +175,7 @@ extern "C" {
 
 void nvfp4_test_wait_fault(uint64_t limit_ns, int withhold) {
   g_wait_limit_ns.store(limit_ns == 0 ? tc_wait_default_ns() : limit_ns);
-  g_wait_hold.store(withhold != 0 ? 1 : 0);
+  g_wait_hold.store(withhold == kHoldOneWarp ? kHoldOneWarp : withhold != 0 ? kHoldLoads : 0);
 }
 
 size_t nvfp4_scales_bytes(int64_t rows, int64_t cols, nvfp4_sf_layout layout) {

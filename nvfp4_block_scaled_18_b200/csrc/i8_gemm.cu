@@ -19,7 +19,9 @@
 //              from TMEM, scaled, transposed through shared memory and stored
 //              in segments of 16 bytes.  Two accumulators alternate, so a tile's
 //              epilogue runs under the next tile's MMAs.
-// Every mbarrier wait is bounded, as in the other tensor-core kernels.
+// Every mbarrier wait is bounded, as in the other tensor-core kernels.  The epilogue's
+// warps meet at a barrier once per tile, so a warp that gave up goes on to the last
+// tile's barrier without working.
 //
 // Bound: the tensor cores, 3.5 POP/s in bursts and 3.15 under the power cap (8192 x
 // 28672 x 8192: 1080 and 1223 us); for a few waves of tiles the filling and the
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int stage = stage_bytes(CG, p.bn);
     int s = 0, issued = 0;
     uint32_t ph = 0;
-    bool ok = !p.hold;
+    bool ok = p.hold != kHoldLoads;
     int tok, ch;
     tile_blocks(p, group, &tok, &ch);
     for (int tile = group; ok && tile < p.num_tiles; tile += groups) {
@@ -240,6 +242,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t* buf = epi + (warp - 4) * 32 * EPI_PITCH;
     const uint32_t quad = (uint32_t)(q * 32) << 16;
     int local = 0;
+    bool ok = true;            // of this warp: the others may not have given up yet
     for (int tile = group; tile < p.num_tiles; tile += groups, ++local) {
       int tok, ch;
       tile_blocks(p, tile, &tok, &ch);
@@ -255,7 +258,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       const float sr = row_in ? (SWAP ? p.w_scales : p.a_scales)[row0 + lane] : 0.0f;
       const float bias_r = SWAP && row_in && p.bias != nullptr ? p.bias[row0 + lane] : 0.0f;
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (!warp_wait<CG == 2>(saddr(&acc_full[b]), (uint32_t)((local >> 1) & 1), ws, p.st)) break;
+      if (p.hold == kHoldOneWarp && warp == 4 && ok) {
+        if (lane == 0) {
+          wait_raise(ws);
+          report_status(p.st, NVFP4_ERR_TIMEOUT);
+        }
+        ok = false;
+      }
+      ok = ok && warp_wait<CG == 2>(saddr(&acc_full[b]), (uint32_t)((local >> 1) & 1), ws, p.st);
+      if (!ok) continue;
       tc_fence_after();
       auto release = [&] {                                // this warp has read its part of the accumulator
         tc_fence_before();

@@ -65,7 +65,9 @@ cudaError_t launch_weight_quant(const void* w, nvfp4_dtype dt, int64_t N, int64_
 // host side): limit_ns bounds every device-side wait; hold != 0 makes the load
 // issuers skip their operand loads, so that the waits run out and the launch
 // reports NVFP4_ERR_TIMEOUT (a test of the timeout path, set through
-// nvfp4_test_wait_fault).
+// nvfp4_test_wait_fault).  kHoldOneWarp, in k_i8_gemm: the loads go on, and one
+// epilogue warp of each CTA gives up at its first tile.
+constexpr int kHoldLoads = 1, kHoldOneWarp = 2;
 struct WaitTest {
   uint64_t limit_ns;
   int hold;

@@ -1,0 +1,44 @@
+"""The tile kernel of the 8-bit integer linear (more tokens than the split-K kernel takes): its waits, its widths, the
+order of its tiles."""
+import time
+
+import pytest
+import torch
+
+import nvfp4_block_scaled_18_b200 as nv
+
+pytestmark = pytest.mark.gpu
+BF, F32, I8 = torch.bfloat16, torch.float32, torch.int8
+ERR_TIMEOUT = 6
+
+
+def operands(M, N, K, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    a = torch.randint(-128, 128, (M, K), dtype=I8, device="cuda", generator=g)
+    w = torch.randint(-128, 128, (N, K), dtype=I8, device="cuda", generator=g)
+    sa, sw = (0.01 + torch.rand(n, device="cuda", generator=g) for n in (M, N))
+    return a, sa, w, sw
+
+
+@pytest.mark.parametrize("M,N,K", [(700, 9000, 256), (777, 11008, 4096), (5000, 6000, 256)])
+def test_one_warp_that_gives_up_stops_no_other(M, N, K):
+    """One output warp of each CTA gives up at its first of several tiles, the others go on: the launch ends, says so,
+    and the next call is right."""
+    a, sa, w, sw = operands(M, N, K)
+    y, st = torch.empty(M, N, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    nv.nvfp4_i8_gemm(a, sa, w, sw, y, dev_status=st)
+    good = y.clone()
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    nv.nvfp4_test_wait_fault(20_000_000, 2)
+    try:
+        t0 = time.perf_counter()
+        nv.nvfp4_i8_gemm(a, sa, w, sw, y, dev_status=st)
+        torch.cuda.synchronize()
+        dt = time.perf_counter() - t0
+    finally:
+        nv.nvfp4_test_wait_fault(0, 0)
+    assert st.item() == ERR_TIMEOUT and dt < 2.0, (st.item(), dt)
+    st.zero_()
+    nv.nvfp4_i8_gemm(a, sa, w, sw, y, dev_status=st)
+    assert st.item() == 0 and torch.equal(y, good)
