@@ -190,12 +190,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (++s == p.stages) { s = 0; ph ^= 1u; }
       }
     }
-    // copies still in flight if a consumer gave up land before the CTA can exit
+    // Copies still in flight if a consumer gave up land before the CTA can exit.  The
+    // leader's barriers count both CTAs' copies, but only of stages that the leader
+    // issued too: the CTA that gave up (either may be first) gives the other's last
+    // ones time to land, copies take microseconds, and neither leaves before both
+    // have come to the cluster's last barrier.
     if (rank == 0) {
       for (int i = max(0, issued - p.stages); i < issued; ++i)
         (void)mbar_drain<CG == 2>(saddr(&full[i % p.stages]), (uint32_t)((i / p.stages) & 1), ws, p.st);
-    } else if (wait_aborted(ws)) {
-      // the leader's barrier counts this CTA's copies: give them time to land (copies take microseconds)
+    }
+    if (wait_aborted(ws)) {
       const uint64_t t0 = globaltimer();
       while (globaltimer() - t0 < 2000000ull) __nanosleep(1000);
     }
