@@ -30,6 +30,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "i8_plan.h"
 #include "i8_tc.cuh"
 #include "kernels.h"
 
@@ -66,23 +67,12 @@ struct Params {
   int M, N, K;        // of the tiles: SWAP has the channels as M and the tokens as N
   int bn;             // columns per tile, a multiple of 32
   int stages;         // of the ring
-  int tok_blocks, ch_blocks;   // blocks of tokens and of channels
-  int group;          // token blocks that W passes by at a time
+  i8::TileOrder order;
   int num_tiles, k_tiles;
   int* st;
   uint64_t wait_ns;
   int hold;
 };
-
-// The tiles' order: groups of token blocks, within a group channel by channel
-// block, tokens fastest.  The CTAs in flight then share W's tiles, and the group's
-// tokens stay in L2 while all of W passes (launch_tiles takes 32 MB of them).
-__device__ __forceinline__ void tile_blocks(const Params& p, int tile, int* tok, int* ch) {
-  const int per = p.group * p.ch_blocks, g = tile / per, r = tile - g * per;
-  const int wide = min(p.group, p.tok_blocks - g * p.group);
-  *ch = r / wide;
-  *tok = g * p.group + r - *ch * wide;
-}
 
 // CG = 2: the copy lands in this CTA, its bytes count on the leader's barrier
 // (the same offset in the even-ranked CTA of the pair).
@@ -171,7 +161,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t ph = 0;
     bool ok = p.hold != kHoldLoads;
     int tok, ch;
-    tile_blocks(p, group, &tok, &ch);
+    i8::tile_blocks(p.order, group, &tok, &ch);
     for (int tile = group; ok && tile < p.num_tiles; tile += groups) {
       const int mb = SWAP ? ch : tok, nb = SWAP ? tok : ch;
       const int a_row = (mb * CG + (int)rank) * BM, w_row = nb * p.bn + (int)rank * (p.bn / CG);
@@ -185,7 +175,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           load_2d<CG>(dst + A_BYTES, &tmB, kt * BK, w_row, bar);
         }
         __syncwarp();
-        if (kt == 0) tile_blocks(p, tile + groups, &tok, &ch);    // the next tile's place, off the ring's critical path
+        if (kt == 0) i8::tile_blocks(p.order, tile + groups, &tok, &ch);    // the next tile's place, off the ring's critical path
         ++issued;
         if (++s == p.stages) { s = 0; ph ^= 1u; }
       }
@@ -249,7 +239,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool ok = true;            // of this warp: the others may not have given up yet
     for (int tile = group; tile < p.num_tiles; tile += groups, ++local) {
       int tok, ch;
-      tile_blocks(p, tile, &tok, &ch);
+      i8::tile_blocks(p.order, tile, &tok, &ch);
       const int mb = SWAP ? ch : tok, nb = SWAP ? tok : ch, b = local & 1;
       const int row0 = (mb * CG + (int)rank) * BM + q * 32, n0 = nb * p.bn, n_end = min(p.N, n0 + p.bn);
       float* ct = cols + b * 2 * BN_MAX;
@@ -404,14 +394,8 @@ cudaError_t launch_tiles(const I8GemmArgs& g, int bn, int num_sms, cudaStream_t 
   p.M = (int)rows; p.N = (int)columns; p.K = (int)g.K; p.bn = bn;
   p.stages = std::min(MAX_STAGES, RING_BYTES / stage_bytes(CG, bn));
   p.num_tiles = (int)(mb * nb); p.k_tiles = (int)((g.K + BK - 1) / BK);
-  // Tokens in groups of 32 MB: 8192 x 28672 x 8192, again and again under the power
-  // cap, takes 1271 us so, 1423 in one group of 67 MB, which W pushes out of L2, and
-  // 1293 in groups of 17 MB, for each of which W comes once from DRAM (8192 x 4096 x
-  // 14336: 337, 374 and 342 us).
-  p.tok_blocks = (int)(SWAP ? nb : mb); p.ch_blocks = (int)(SWAP ? mb : nb);
-  const int64_t block_bytes = (int64_t)(SWAP ? bn : BM * CG) * g.K;
-  const int64_t most = std::max<int64_t>(1, (32ll << 20) / block_bytes), groups = (p.tok_blocks + most - 1) / most;
-  p.group = (int)((p.tok_blocks + groups - 1) / groups);
+  p.order.tok_blocks = (int)(SWAP ? nb : mb); p.order.ch_blocks = (int)(SWAP ? mb : nb);
+  p.order.group = i8::token_group(p.order.tok_blocks, (int64_t)(SWAP ? bn : BM * CG) * g.K);
   p.st = g.st;
   const WaitTest wt = wait_test();
   p.wait_ns = wt.limit_ns; p.hold = wt.hold;

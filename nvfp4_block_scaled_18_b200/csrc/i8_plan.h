@@ -1,0 +1,42 @@
+// Choices of the 8-bit linear's launchers and the order of its tiles, in plain
+// C++: they compile without CUDA, so that they can be checked without a GPU.
+#pragma once
+
+#include <algorithm>
+#include <cstdint>
+
+#ifdef __CUDACC__
+#define NVFP4_HD __host__ __device__ __forceinline__
+#else
+#define NVFP4_HD inline
+#endif
+
+namespace nvfp4 {
+namespace i8 {
+
+// The tiles' order: groups of token blocks, within a group channel by channel
+// block, tokens fastest.  The CTAs in flight then share W's tiles, and the group's
+// tokens stay in L2 while all of W passes.  A tile beyond the last one has no place:
+// what it is given is not used, only defined.
+struct TileOrder {
+  int tok_blocks, ch_blocks;   // blocks of tokens and of channels
+  int group;                   // token blocks that W passes by at a time
+};
+NVFP4_HD void tile_blocks(const TileOrder& o, int tile, int* tok, int* ch) {
+  const int per = o.group * o.ch_blocks, g = tile / per, r = tile - g * per;
+  const int left = o.tok_blocks - g * o.group, wide = left >= o.group ? o.group : left > 1 ? left : 1;
+  *ch = r / wide;
+  *tok = g * o.group + r - *ch * wide;
+}
+
+// Tokens in groups of 32 MB: 8192 x 28672 x 8192, again and again under the power
+// cap, takes 1271 us so, 1423 in one group of 67 MB, which W pushes out of L2, and
+// 1293 in groups of 17 MB, for each of which W comes once from DRAM (8192 x 4096 x
+// 14336: 337, 374 and 342 us).  block_bytes: of a block of tokens.
+inline int token_group(int tok_blocks, int64_t block_bytes) {
+  const int64_t most = std::max<int64_t>(1, (32ll << 20) / block_bytes), groups = (tok_blocks + most - 1) / most;
+  return (int)((tok_blocks + groups - 1) / groups);
+}
+
+}  // namespace i8
+}  // namespace nvfp4

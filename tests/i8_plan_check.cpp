@@ -1,0 +1,45 @@
+// Questions about csrc/i8_plan.h, one a line on standard input, answers on standard output:
+//   order TOK_BLOCKS CH_BLOCKS BLOCK_BYTES GRID   -> group, and every tile visited once by GRID walkers that look one
+//                                                    tile ahead ("ok" or what is wrong)
+#include <cstdio>
+#include <cstring>
+#include <vector>
+
+#include "i8_plan.h"
+
+using namespace nvfp4::i8;
+
+static void order(int tok_blocks, int ch_blocks, int64_t block_bytes, int grid) {
+  TileOrder o{tok_blocks, ch_blocks, token_group(tok_blocks, block_bytes)};
+  const int tiles = tok_blocks * ch_blocks;
+  std::vector<int> seen((size_t)tiles);
+  for (int first = 0; first < std::min(grid, tiles); ++first) {
+    int tok, ch;
+    tile_blocks(o, first, &tok, &ch);
+    for (int tile = first; tile < tiles; tile += grid) {
+      if (tok < 0 || tok >= tok_blocks || ch < 0 || ch >= ch_blocks) {
+        std::printf("%d tile %d at %d, %d\n", o.group, tile, tok, ch);
+        return;
+      }
+      ++seen[(size_t)(tok * ch_blocks + ch)];
+      tile_blocks(o, tile + grid, &tok, &ch);     // ahead, beyond the last one too
+    }
+  }
+  for (int i = 0; i < tiles; ++i)
+    if (seen[(size_t)i] != 1) {
+      std::printf("%d block %d visited %d times\n", o.group, i, seen[(size_t)i]);
+      return;
+    }
+  std::printf("%d ok\n", o.group);
+}
+
+int main() {
+  char what[16];
+  while (std::scanf("%15s", what) == 1) {
+    long long a, b, c, d;
+    if (!std::strcmp(what, "order") && std::scanf("%lld %lld %lld %lld", &a, &b, &c, &d) == 4) order((int)a, (int)b, c, (int)d);
+    else return 2;
+    std::fflush(stdout);
+  }
+  return 0;
+}

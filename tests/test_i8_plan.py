@@ -1,0 +1,42 @@
+"""The host side of the 8-bit linear's launchers (csrc/i8_plan.h), compiled for the CPU with the undefined-behaviour
+checks on: integer division by zero and overflow end the program."""
+import os
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "nvfp4_block_scaled_18_b200", "csrc")
+
+
+@pytest.fixture(scope="module")
+def ask(tmp_path_factory):
+    """ask(lines) -> the answers, one a line."""
+    exe = str(tmp_path_factory.mktemp("i8_plan") / "i8_plan_check")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-fsanitize=integer-divide-by-zero,signed-integer-overflow",
+                    "-fno-sanitize-recover=all", "-I" + CSRC, os.path.join(ROOT, "tests", "i8_plan_check.cpp"), "-o", exe],
+                   check=True)
+
+    def run(lines):
+        r = subprocess.run([exe], input="\n".join(lines) + "\n", capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr
+        out = r.stdout.splitlines()
+        assert len(out) == len(lines)
+        return out
+
+    return run
+
+
+def test_every_tile_once(ask):
+    """The walk of the CTA pairs over the tiles, each looking up its next place while it works on the present one, as the
+    loads' issuer does: also where the last tile ends a group, and where the last group is short."""
+    lines = [f"order {tok} {ch} {size} {grid}"
+             for tok in (1, 2, 3, 5, 16, 17, 32, 65) for ch in (1, 2, 7, 43, 112)
+             for size in (4096, 256 * 8192, 256 * 65536, 256 * 131056) for grid in (1, 2, 66, 74)]
+    for line, answer in zip(lines, ask(lines)):
+        assert answer.split()[1:] == ["ok"], (line, answer)
+
+
+def test_token_groups(ask):
+    """Groups of at most 32 MB, as even as they come, and one block at least."""
+    assert [a.split()[0] for a in ask(["order 32 112 2097152 74", "order 5 10 16777216 74", "order 3 2 67108864 74"])] == ["16", "2", "1"]
