@@ -246,11 +246,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int c = et; c < p.bn; c += 32 * EPI_WARPS) {
         const bool in = n0 + c < p.N;
         ct[c] = in ? (SWAP ? p.a_scales : p.w_scales)[n0 + c] : 0.0f;
-        ct[BN_MAX + c] = !SWAP && in && p.bias != nullptr ? p.bias[n0 + c] : 0.0f;
+        ct[BN_MAX + c] = !SWAP && in && p.bias != nullptr ? p.bias[n0 + c] : kNoBias;
       }
       const bool row_in = row0 + lane < p.M;
       const float sr = row_in ? (SWAP ? p.w_scales : p.a_scales)[row0 + lane] : 0.0f;
-      const float bias_r = SWAP && row_in && p.bias != nullptr ? p.bias[row0 + lane] : 0.0f;
+      const float bias_r = SWAP && row_in && p.bias != nullptr ? p.bias[row0 + lane] : kNoBias;
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (p.hold == kHoldOneWarp && warp == 4 && ok) {
         if (lane == 0) {

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncwarp();
   // this thread's column of Y and its scale, loaded while the MMAs run
   const int q = warp & 3, half = warp >> 2, row = q * 32 + lane, n = n0 + row;
-  float sw = 0.0f, bias = 0.0f;
+  float sw = 0.0f, bias = kNoBias;
   if (n < p.N) {
     sw = p.w_scales[n];
     if (p.bias != nullptr) bias = p.bias[n];

@@ -47,6 +47,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, WaitSta
   return ok != 0;
 }
 
+// What is added where there is no bias: x + -0 is x, the sign of a zero included.
+constexpr float kNoBias = -0.0f;
+
 // kind::i8: int8 A and B (both K-major), int32 accumulator, M rows, N columns.
 __device__ __forceinline__ uint32_t idesc_i8(int m, int n) {
   return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);

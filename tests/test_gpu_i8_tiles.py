@@ -42,3 +42,16 @@ def test_one_warp_that_gives_up_stops_no_other(M, N, K):
     st.zero_()
     nv.nvfp4_i8_gemm(a, sa, w, sw, y, dev_status=st)
     assert st.item() == 0 and torch.equal(y, good)
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("M,N,K", [(1, 100, 64), (4, 100, 64), (16, 300, 1024), (100, 300, 2048), (200, 512, 8192),
+                                   (300, 500, 256), (1031, 4096, 2064)])
+def test_without_a_bias_nothing_is_added(M, N, K, out):
+    """A product of -0 stays -0 in every kernel: fl32(acc) = +0, times a negative channel scale."""
+    a, sa, w, sw = operands(M, N, K)
+    y = torch.empty(M, N, dtype=out, device="cuda")
+    nv.nvfp4_i8_gemm(torch.zeros_like(a), sa, w, -sw, y)
+    assert (y == 0).all() and torch.signbit(y).all()
+    nv.nvfp4_i8_gemm(torch.zeros_like(a), sa, w, -sw, y, bias=torch.zeros(N, device="cuda"))
+    assert (y == 0).all() and not torch.signbit(y).any()          # -0 + 0
