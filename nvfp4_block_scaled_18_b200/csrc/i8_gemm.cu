@@ -39,8 +39,8 @@ using namespace tc;
 namespace {
 
 constexpr int BM = 128;                 // rows of A per CTA
-constexpr int BK = 128;                 // bytes (= elements) of K per stage: one swizzle row
-constexpr int BN_MAX = 256;             // columns per tile, at most
+using i8::BK;                           // bytes (= elements) of K per stage: one swizzle row
+using i8::BN_MAX;                       // columns per tile, at most
 constexpr int A_BYTES = BM * BK;
 constexpr int THREADS = 384;
 constexpr int EPI_WARPS = 8;
@@ -442,27 +442,12 @@ cudaError_t launch_i8_gemm(const I8GemmArgs& g, int num_sms, cudaStream_t stream
   // Up to 128 tokens W's rows fill the tensor cores' M better than the tokens do
   // (128 x 5120 x 5120: 11.6 us, tiles of 256 tokens x 96 columns 13.8).
   if (g.M <= 128) return launch_i8_gemm_few(g, num_sms, stream);
-  // Beyond, tiles of a pair of CTAs, 256 tokens x bn channels or 256 channels x bn
-  // tokens, by an estimate: a K-slice takes 84 ns + 1 ns a column, and 222 ns at
-  // least (measured, 128 to 256 columns); filling, the last epilogue and the launch
-  // come on top (777 x 11008 x 4096: 160 tokens wide 32.4 us, 224 channels wide
-  // 35.6; 512 x 4096 x 14336: 128 channels wide 29.4, 224 wide 33.0).  Up to 256
-  // tokens splitting K instead can win (256 x 5120 x 27648: 40 us, tiles 52 us;
-  // 256 x 4096 x 4096: 13.7 and 11.5 us).
-  const int64_t k_tiles = (g.K + BK - 1) / BK, pairs = std::max(1, num_sms / 2);
-  double best = 0.0;
-  int bn = 0;
-  bool swap = false;
-  for (int side = 0; side < 2; ++side) {
-    const int64_t rows = side ? g.N : g.M, columns = side ? g.M : g.N, mb = (rows + 2 * BM - 1) / (2 * BM);
-    for (int c = 32; c <= BN_MAX; c += 32) {
-      const int64_t waves = (mb * ((columns + c - 1) / c) + pairs - 1) / pairs;
-      const double ns = 5000.0 + 8.0 * c + (double)(waves * k_tiles) * std::max(222.0, 84.0 + c) + (side ? 500.0 : 0.0);
-      if (bn == 0 || ns < best || (!side && ns <= best)) { best = ns; bn = c; swap = side != 0; }
-    }
-  }
-  if (g.M <= 256 && i8_gemm_few_ns(g.M, g.N, g.K, num_sms) < best) return launch_i8_gemm_few(g, num_sms, stream);
-  return swap ? launch_tiles<2, true>(g, bn, num_sms, stream) : launch_tiles<2, false>(g, bn, num_sms, stream);
+  // Beyond, tiles of a pair of CTAs by an estimate.  Up to 256 tokens splitting K
+  // instead can win (256 x 5120 x 27648: 40 us, tiles 52 us; 256 x 4096 x 4096: 13.7
+  // and 11.5 us).
+  const i8::Tiles t = i8::choose_tiles(g.M, g.N, g.K, num_sms);
+  if (g.M <= 256 && i8_gemm_few_ns(g.M, g.N, g.K, num_sms) < t.ns) return launch_i8_gemm_few(g, num_sms, stream);
+  return t.swap ? launch_tiles<2, true>(g, t.bn, num_sms, stream) : launch_tiles<2, false>(g, t.bn, num_sms, stream);
 }
 
 }  // namespace nvfp4

@@ -14,6 +14,33 @@
 namespace nvfp4 {
 namespace i8 {
 
+constexpr int BK = 128;       // bytes (= elements) of K per stage of the tensor-core kernels
+constexpr int BN_MAX = 256;   // columns per tile, at most
+
+// Tiles of a pair of CTAs: 256 tokens x bn channels, or (swap) 256 channels x bn
+// tokens, by an estimate.  A K-slice takes 84 ns + 1 ns a column, and 222 ns at
+// least (measured, 128 to 256 columns); filling, the last epilogue and the launch
+// come on top (777 x 11008 x 4096: 160 tokens wide 32.4 us, 224 channels wide 35.6;
+// 512 x 4096 x 14336: 128 channels wide 29.4, 224 wide 33.0).
+struct Tiles {
+  int bn;
+  bool swap;
+  double ns;                  // the estimate
+};
+inline Tiles choose_tiles(int64_t M, int64_t N, int64_t K, int num_sms) {
+  const int64_t k_tiles = (K + BK - 1) / BK, pairs = std::max(1, num_sms / 2);
+  Tiles best{0, false, 0.0};
+  for (int side = 0; side < 2; ++side) {
+    const int64_t rows = side ? N : M, columns = side ? M : N, mb = (rows + 255) / 256;
+    for (int c = 32; c <= BN_MAX; c += 32) {
+      const int64_t waves = (mb * ((columns + c - 1) / c) + pairs - 1) / pairs;
+      const double ns = 5000.0 + 8.0 * c + (double)(waves * k_tiles) * std::max(222.0, 84.0 + c) + (side ? 500.0 : 0.0);
+      if (best.bn == 0 || ns < best.ns || (!side && ns <= best.ns)) best = Tiles{c, side != 0, ns};
+    }
+  }
+  return best;
+}
+
 // The tiles' order: groups of token blocks, within a group channel by channel
 // block, tokens fastest.  The CTAs in flight then share W's tiles, and the group's
 // tokens stay in L2 while all of W passes.  A tile beyond the last one has no place:

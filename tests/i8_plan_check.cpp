@@ -1,6 +1,7 @@
 // Questions about csrc/i8_plan.h, one a line on standard input, answers on standard output:
 //   order TOK_BLOCKS CH_BLOCKS BLOCK_BYTES GRID   -> group, and every tile visited once by GRID walkers that look one
 //                                                    tile ahead ("ok" or what is wrong)
+//   tiles M N K SMS                               -> bn, swap, token blocks, their group, tiles
 #include <cstdio>
 #include <cstring>
 #include <vector>
@@ -33,11 +34,19 @@ static void order(int tok_blocks, int ch_blocks, int64_t block_bytes, int grid) 
   std::printf("%d ok\n", o.group);
 }
 
+static void tiles(int64_t M, int64_t N, int64_t K, int sms) {
+  const Tiles t = choose_tiles(M, N, K, sms);
+  const int64_t tok = t.swap ? (M + t.bn - 1) / t.bn : (M + 255) / 256, ch = t.swap ? (N + 255) / 256 : (N + t.bn - 1) / t.bn;
+  std::printf("%d %d %lld %d %lld\n", t.bn, t.swap ? 1 : 0, (long long)tok, token_group((int)tok, (t.swap ? t.bn : 256) * K),
+              (long long)(tok * ch));
+}
+
 int main() {
   char what[16];
   while (std::scanf("%15s", what) == 1) {
     long long a, b, c, d;
     if (!std::strcmp(what, "order") && std::scanf("%lld %lld %lld %lld", &a, &b, &c, &d) == 4) order((int)a, (int)b, c, (int)d);
+    else if (!std::strcmp(what, "tiles") && std::scanf("%lld %lld %lld %lld", &a, &b, &c, &d) == 4) tiles(a, b, c, (int)d);
     else return 2;
     std::fflush(stdout);
   }

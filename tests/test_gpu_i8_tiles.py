@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import nvfp4_block_scaled_18_b200 as nv
+from i8_cases import GROUPS, TILES
 
 pytestmark = pytest.mark.gpu
 BF, F32, I8 = torch.bfloat16, torch.float32, torch.int8
@@ -55,3 +56,33 @@ def test_without_a_bias_nothing_is_added(M, N, K, out):
     assert (y == 0).all() and torch.signbit(y).all()
     nv.nvfp4_i8_gemm(torch.zeros_like(a), sa, w, -sw, y, bias=torch.zeros(N, device="cuda"))
     assert (y == 0).all() and not torch.signbit(y).any()          # -0 + 0
+
+
+def plain(a, sa, w, sw, bias):
+    """float32 result before the rounding to the output type: sums in 64 bits over runs of K, exact."""
+    acc = torch.zeros(a.shape[0], w.shape[0], dtype=torch.float64, device="cuda")
+    for k in range(0, a.shape[1], 8192):
+        acc += a[:, k:k + 8192].double() @ w[:, k:k + 8192].double().T
+    y = acc.float() * sa[:, None] * sw
+    return y if bias is None else y + bias
+
+
+def check(M, N, K, out, with_bias, pad):
+    """Exact, and nothing written beside the output; rows of Y `pad` elements further apart than they are long."""
+    a, sa, w, sw = operands(M, N, K, M + N + K)
+    bias = torch.randn(N, device="cuda") if with_bias else None
+    buf, st = torch.full((M + 1, N + pad), -77.0, dtype=out, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    nv.nvfp4_i8_gemm(a, sa, w, sw, buf[:M, :N], bias, dev_status=st)
+    assert torch.equal(buf[:M, :N], plain(a, sa, w, sw, bias).to(out)) and st.item() == 0
+    assert (buf[M:] == -77.0).all() and (buf[:, N:] == -77.0).all()
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("M,N,K,bn,swap", TILES)
+def test_every_width(M, N, K, bn, swap, out):
+    check(M, N, K, out, M % 2 == 0, -N % 8 if M % 3 else 3)
+
+
+@pytest.mark.parametrize("M,N,K,tok,group", GROUPS)
+def test_groups_of_tokens(M, N, K, tok, group):
+    check(M, N, K, BF, True, 0)

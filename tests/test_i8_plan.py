@@ -5,6 +5,8 @@ import subprocess
 
 import pytest
 
+from i8_cases import GROUPS, TILES
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "nvfp4_block_scaled_18_b200", "csrc")
 
@@ -40,3 +42,21 @@ def test_every_tile_once(ask):
 def test_token_groups(ask):
     """Groups of at most 32 MB, as even as they come, and one block at least."""
     assert [a.split()[0] for a in ask(["order 32 112 2097152 74", "order 5 10 16777216 74", "order 3 2 67108864 74"])] == ["16", "2", "1"]
+
+
+def test_cases_reach_every_width(ask):
+    """The GPU tests' shapes: every width that the estimate takes, from either side, and short last groups."""
+    got = [[int(v) for v in a.split()] for a in ask([f"tiles {m} {n} {k} 148" for m, n, k, _, _ in TILES])]
+    assert [(g[0], bool(g[1])) for g in got] == [(bn, swap) for *_, bn, swap in TILES]
+    assert {bn for *_, bn, swap in TILES if not swap} == set(range(32, 257, 32))
+    assert {bn for *_, bn, swap in TILES if swap} == set(range(64, 225, 32))
+    got = [[int(v) for v in a.split()] for a in ask([f"tiles {m} {n} {k} 148" for m, n, k, _, _ in GROUPS])]
+    assert [(g[2], g[3]) for g in got] == [(tok, group) for *_, tok, group in GROUPS]
+    assert all(tok > group and tok % group for *_, tok, group in GROUPS)
+
+
+def test_widths_taken(ask):
+    """Over the whole range of sizes no other width is taken than those the cases have."""
+    sizes = [(m, n, k) for m in range(257, 8200, 379) for n in range(64, 28700, 1237) for k in (64, 528, 1552, 4096, 8192, 27648)]
+    taken = {tuple(a.split()[:2]) for a in ask([f"tiles {m} {n} {k} 148" for m, n, k in sizes])}
+    assert taken <= {(str(bn), str(int(swap))) for *_, bn, swap in TILES}
