@@ -24,6 +24,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "i8_plan.h"
 #include "i8_tc.cuh"
 #include "kernels.h"
 
@@ -285,17 +286,18 @@ int clusters_at_once(int ks, int num_sms) {
   static std::atomic<int> cache[16][9];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) dev = 16;
-  const int known = dev < 16 ? cache[dev][ks].load(std::memory_order_relaxed) : 0;
-  if (known > 0) return known;
-  static SmemOnce once;
-  cudaLaunchAttribute at[2];
-  const cudaLaunchConfig_t cfg = few_config<NP, 1, BF16OUT>((unsigned)(num_sms * 8 / ks * ks), ks, nullptr, at);
-  int n = 0;
-  if (once.set(k_i8_few<NP, 1, BF16OUT>, Cfg<NP, 1>::SMEM) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, k_i8_few<NP, 1, BF16OUT>, &cfg) != cudaSuccess || n <= 0)
-    n = std::max(1, num_sms / ks / 2);            // not known: a low guess, which only splits K less
-  if (dev < 16) cache[dev][ks].store(n, std::memory_order_relaxed);
-  return n;
+  // not known: a low guess, which only splits K less
+  return i8::asked_once(dev < 16 ? &cache[dev][ks] : nullptr, std::max(1, num_sms / ks / 2), [&] {
+    static SmemOnce once;
+    cudaLaunchAttribute at[2];
+    const cudaLaunchConfig_t cfg = few_config<NP, 1, BF16OUT>((unsigned)(num_sms * 8 / ks * ks), ks, nullptr, at);
+    int n = 0;
+    if (once.set(k_i8_few<NP, 1, BF16OUT>, Cfg<NP, 1>::SMEM) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, k_i8_few<NP, 1, BF16OUT>, &cfg) == cudaSuccess)
+      return n;
+    (void)cudaGetLastError();                     // the call goes on without the answer
+    return 0;
+  });
 }
 
 // The largest split of K whose clusters fit one wave (16 x 4096 x 14336 in 32

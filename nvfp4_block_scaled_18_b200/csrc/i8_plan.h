@@ -3,6 +3,7 @@
 #pragma once
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #ifdef __CUDACC__
@@ -63,6 +64,17 @@ NVFP4_HD void tile_blocks(const TileOrder& o, int tile, int* tok, int* ch) {
 inline int token_group(int tok_blocks, int64_t block_bytes) {
   const int64_t most = std::max<int64_t>(1, (32ll << 20) / block_bytes), groups = (tok_blocks + most - 1) / most;
   return (int)((tok_blocks + groups - 1) / groups);
+}
+
+// An answer of the device that does not change, asked once.
+template <typename Ask>
+int asked_once(std::atomic<int>* slot, int guess, Ask ask) {
+  int n = slot != nullptr ? slot->load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  n = ask();
+  if (n <= 0) return guess;             // not known: for this call alone
+  if (slot != nullptr) slot->store(n, std::memory_order_relaxed);
+  return n;
 }
 
 }  // namespace i8

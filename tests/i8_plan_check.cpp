@@ -2,6 +2,8 @@
 //   order TOK_BLOCKS CH_BLOCKS BLOCK_BYTES GRID   -> group, and every tile visited once by GRID walkers that look one
 //                                                    tile ahead ("ok" or what is wrong)
 //   tiles M N K SMS                               -> bn, swap, token blocks, their group, tiles
+//   held FIRST SECOND                             -> three answers of asked_once (guess 5) where the device gives
+//                                                    FIRST, then SECOND, and how often it was asked
 #include <cstdio>
 #include <cstring>
 #include <vector>
@@ -41,12 +43,21 @@ static void tiles(int64_t M, int64_t N, int64_t K, int sms) {
               (long long)(tok * ch));
 }
 
+static void held(int first, int second) {
+  std::atomic<int> slot{0};
+  int asked = 0;
+  auto ask = [&] { return ++asked == 1 ? first : second; };
+  for (int i = 0; i < 3; ++i) std::printf("%d ", asked_once(&slot, 5, ask));
+  std::printf("%d\n", asked);
+}
+
 int main() {
   char what[16];
   while (std::scanf("%15s", what) == 1) {
     long long a, b, c, d;
     if (!std::strcmp(what, "order") && std::scanf("%lld %lld %lld %lld", &a, &b, &c, &d) == 4) order((int)a, (int)b, c, (int)d);
     else if (!std::strcmp(what, "tiles") && std::scanf("%lld %lld %lld %lld", &a, &b, &c, &d) == 4) tiles(a, b, c, (int)d);
+    else if (!std::strcmp(what, "held") && std::scanf("%lld %lld", &a, &b) == 2) held((int)a, (int)b);
     else return 2;
     std::fflush(stdout);
   }

@@ -60,3 +60,8 @@ def test_widths_taken(ask):
     sizes = [(m, n, k) for m in range(257, 8200, 379) for n in range(64, 28700, 1237) for k in (64, 528, 1552, 4096, 8192, 27648)]
     taken = {tuple(a.split()[:2]) for a in ask([f"tiles {m} {n} {k} 148" for m, n, k in sizes])}
     assert taken <= {(str(bn), str(int(swap))) for *_, bn, swap in TILES}
+
+
+def test_failed_query_is_asked_again(ask):
+    """A query that fails gives a guess for that call alone; an answer is kept."""
+    assert ask(["held 33 7", "held 0 33", "held -1 -1"]) == ["33 33 33 1", "5 33 33 2", "5 5 5 3"]
