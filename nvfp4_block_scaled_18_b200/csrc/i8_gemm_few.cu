@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-template <int NP, int CTAS, bool BF16OUT>
+template <int NP, int CTAS>
 cudaLaunchConfig_t few_config(unsigned grid, int ks, cudaStream_t stream, cudaLaunchAttribute (&at)[2]) {
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -278,22 +278,30 @@ cudaLaunchConfig_t few_config(unsigned grid, int ks, cudaStream_t stream, cudaLa
   return cfg;
 }
 
-// Clusters of ks CTAs, one per SM, that the device holds at once: asked once per
-// device and split, since the GPCs' sizes differ (148 SMs held 33 clusters of four,
-// 132 CTAs; 36 of them took two waves, 64 x 4500 x 28672 41 us, in three parts 26).
-template <int NP, bool BF16OUT>
+// Stands in for k_i8_few in questions of occupancy, never launched: the device counts
+// one CTA per SM for any kernel that allocates tensor memory, and two run.
+__global__ void __launch_bounds__(THREADS) k_few_shape() {}
+SmemOnce shape_once;
+
+// Clusters of ks CTAs, CTAS per SM, that the device holds at once: asked once per
+// device and split, since the GPCs' sizes differ (148 SMs held 33 clusters of four
+// at one CTA per SM, 132 CTAs, and 71 at two; 36 of them at one took two waves, 64 x
+// 4500 x 28672 41 us, in three parts 26).  The answer is what fits, not what the
+// device achieves each time: 56 clusters of five at two per SM still take a second
+// wave (5 x 7168 x 14336 21 us, 57 tiles in four parts 18.8).
+template <int NP, int CTAS>
 int clusters_at_once(int ks, int num_sms) {
   static std::atomic<int> cache[16][9];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) dev = 16;
   // not known: a low guess, which only splits K less
-  return i8::asked_once(dev < 16 ? &cache[dev][ks] : nullptr, std::max(1, num_sms / ks / 2), [&] {
-    static SmemOnce once;
+  return i8::asked_once(dev < 16 ? &cache[dev][ks] : nullptr, std::max(1, num_sms * CTAS / ks / 2), [&] {
     cudaLaunchAttribute at[2];
-    const cudaLaunchConfig_t cfg = few_config<NP, 1, BF16OUT>((unsigned)(num_sms * 8 / ks * ks), ks, nullptr, at);
+    cudaLaunchConfig_t cfg = few_config<NP, CTAS>((unsigned)(num_sms * 8 / ks * ks), ks, nullptr, at);
+    cfg.dynamicSmemBytes += NP * 4;               // the static part
     int n = 0;
-    if (once.set(k_i8_few<NP, 1, BF16OUT>, Cfg<NP, 1>::SMEM) == cudaSuccess &&
-        cudaOccupancyMaxActiveClusters(&n, k_i8_few<NP, 1, BF16OUT>, &cfg) == cudaSuccess)
+    if (shape_once.set(k_few_shape, 232448) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, k_few_shape, &cfg) == cudaSuccess)
       return n;
     (void)cudaGetLastError();                     // the call goes on without the answer
     return 0;
@@ -301,16 +309,16 @@ int clusters_at_once(int ks, int num_sms) {
 }
 
 // The largest split of K whose clusters fit one wave (16 x 4096 x 14336 in 32
-// clusters of eight 12.4 us, of four 13.7), whose partial sums fit and
-// which leaves a CTA enough steps to pay for joining them: above 32 tokens ten
-// (128 x 4096 x 4096: 10.1 us split in 3, 10.6 in 4).
-template <int NP, int CTAS, bool BF16OUT>
+// clusters of eight 12.4 us, of four 13.7; 5 x 5888 x 14336 in 46 clusters of six,
+// one too many, 22.1 us, of five 15.8), whose partial sums fit and which leaves a CTA
+// enough steps to pay for joining them: above 32 tokens ten (128 x 4096 x 4096: 10.1
+// us split in 3, 10.6 in 4).  At two CTAs per SM not seven: 37 clusters of them are no
+// faster than 37 of six (5 x 4736 x 14336: 13.8 and 13.5 us, x 2048 5.4 and 5.0).
+template <int NP, int CTAS>
 int choose_ks(int64_t M, int64_t tiles, int k_steps, int num_sms) {
-  for (int k = 8; k >= 2; --k)
-    if (tiles * k <= (int64_t)num_sms * CTAS && k * (NP > 32 ? 10 : 1) <= k_steps && Cfg<NP, CTAS>::fits((int)M, k) &&
-        tiles * 10 <= (int64_t)clusters_at_once<NP, BF16OUT>(k, num_sms) * (CTAS == 2 ? 22 : 10))   // two per SM leave fewer SMs over
-      return k;
-  return 1;
+  return i8::split_of_k(tiles, k_steps, NP > 32 ? 10 : 1,
+                        [&](int k) { return !(CTAS == 2 && k == 7) && Cfg<NP, CTAS>::fits((int)M, k); },
+                        [&](int k) { return clusters_at_once<NP, CTAS>(k, num_sms); });
 }
 
 template <int NP, int CTAS, bool BF16OUT>
@@ -318,7 +326,7 @@ cudaError_t launch_np(const I8GemmArgs& g, int num_sms, cudaStream_t stream) {
   using C = Cfg<NP, CTAS>;
   const int64_t tiles = (g.N + W_ROWS - 1) / W_ROWS;
   const int k_steps = (int)((g.K + BK - 1) / BK);
-  const int ks = choose_ks<NP, CTAS, BF16OUT>(g.M, tiles, k_steps, num_sms);
+  const int ks = choose_ks<NP, CTAS>(g.M, tiles, k_steps, num_sms);
   if (tiles * ks > INT32_MAX) return cudaErrorNotSupported;
   CUtensorMap tmW, tmX;
   if (!encode_i8_map(&tmW, g.w, g.N, g.K, g.ldw, W_ROWS) || !encode_i8_map(&tmX, g.a, g.M, g.K, g.lda, NP))
@@ -335,7 +343,7 @@ cudaError_t launch_np(const I8GemmArgs& g, int num_sms, cudaStream_t stream) {
   cudaError_t e = once.set(kern, C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute at[2];
-  const cudaLaunchConfig_t cfg = few_config<NP, CTAS, BF16OUT>((unsigned)(tiles * ks), ks, stream, at);
+  const cudaLaunchConfig_t cfg = few_config<NP, CTAS>((unsigned)(tiles * ks), ks, stream, at);
   return cudaLaunchKernelEx(&cfg, kern, tmW, tmX, p);
 }
 
@@ -364,7 +372,7 @@ cudaError_t launch_out(const I8GemmArgs& g, int num_sms, cudaStream_t stream) {
 
 double i8_gemm_few_ns(int64_t M, int64_t N, int64_t K, int num_sms) {
   const int64_t tiles = (N + W_ROWS - 1) / W_ROWS;
-  const int k_steps = (int)((K + BK - 1) / BK), ks = choose_ks<256, 1, true>(M, tiles, k_steps, num_sms);
+  const int k_steps = (int)((K + BK - 1) / BK), ks = choose_ks<256, 1>(M, tiles, k_steps, num_sms);
   const int64_t waves = (tiles * ks + num_sms - 1) / num_sms;
   return 10000.0 + 460.0 * (double)waves * (double)((k_steps + ks - 1) / ks);
 }

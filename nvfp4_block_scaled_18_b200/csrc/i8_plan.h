@@ -66,6 +66,16 @@ inline int token_group(int tok_blocks, int64_t block_bytes) {
   return (int)((tok_blocks + groups - 1) / groups);
 }
 
+// k_i8_few: the largest split of K, up to eight CTAs a cluster, that leaves each CTA
+// `least` steps of K to pay for joining them, whose partial sums fit (fits(k)) and
+// whose clusters, one a tile, all run at once: the device holds held(k) of them.
+template <typename Fits, typename Held>
+int split_of_k(int64_t tiles, int k_steps, int least, Fits fits, Held held) {
+  for (int k = 8; k >= 2; --k)
+    if (k * least <= k_steps && fits(k) && tiles <= held(k)) return k;
+  return 1;
+}
+
 // An answer of the device that does not change, asked once.
 template <typename Ask>
 int asked_once(std::atomic<int>* slot, int guess, Ask ask) {

@@ -2,6 +2,8 @@
 //   order TOK_BLOCKS CH_BLOCKS BLOCK_BYTES GRID   -> group, and every tile visited once by GRID walkers that look one
 //                                                    tile ahead ("ok" or what is wrong)
 //   tiles M N K SMS                               -> bn, swap, token blocks, their group, tiles
+//   split TILES K_STEPS LEAST LARGEST HELD2 .. HELD8 -> split of K where up to LARGEST parts fit and the device holds
+//                                                    HELDk clusters of k, and the number of clusters that it holds
 //   held FIRST SECOND                             -> three answers of asked_once (guess 5) where the device gives
 //                                                    FIRST, then SECOND, and how often it was asked
 #include <cstdio>
@@ -43,6 +45,14 @@ static void tiles(int64_t M, int64_t N, int64_t K, int sms) {
               (long long)(tok * ch));
 }
 
+static void split(int64_t tiles, int k_steps, int least, int largest) {
+  int n[9], used = 0;
+  for (int k = 2; k <= 8; ++k)
+    if (std::scanf("%d", &n[k]) != 1) return;
+  const int ks = split_of_k(tiles, k_steps, least, [&](int k) { return k <= largest; }, [&](int k) { used = n[k]; return n[k]; });
+  std::printf("%d %d\n", ks, ks == 1 ? 0 : used);
+}
+
 static void held(int first, int second) {
   std::atomic<int> slot{0};
   int asked = 0;
@@ -58,6 +68,7 @@ int main() {
     if (!std::strcmp(what, "order") && std::scanf("%lld %lld %lld %lld", &a, &b, &c, &d) == 4) order((int)a, (int)b, c, (int)d);
     else if (!std::strcmp(what, "tiles") && std::scanf("%lld %lld %lld %lld", &a, &b, &c, &d) == 4) tiles(a, b, c, (int)d);
     else if (!std::strcmp(what, "held") && std::scanf("%lld %lld", &a, &b) == 2) held((int)a, (int)b);
+    else if (!std::strcmp(what, "split") && std::scanf("%lld %lld %lld %lld", &a, &b, &c, &d) == 4) split(a, (int)b, (int)c, (int)d);
     else return 2;
     std::fflush(stdout);
   }

@@ -65,3 +65,18 @@ def test_widths_taken(ask):
 def test_failed_query_is_asked_again(ask):
     """A query that fails gives a guess for that call alone; an answer is kept."""
     assert ask(["held 33 7", "held 0 33", "held -1 -1"]) == ["33 33 33 1", "5 33 33 2", "5 5 5 3"]
+
+
+def test_split_runs_in_one_wave(ask):
+    """K is split as far as the clusters of all tiles are held at once, with the numbers of clusters of 2 to 8 that 148
+    SMs held at one CTA per SM and at two."""
+    for at_once in ((74, 45, 33, 26, 22, 15, 15), (148, 93, 71, 56, 45, 37, 33)):
+        lines = [f"split {t} 112 1 8 " + " ".join(map(str, at_once)) for t in range(1, 160)]
+        for tiles, answer in enumerate(ask(lines), 1):
+            ks, held = map(int, answer.split())
+            assert ks == max([1] + [k for k in range(2, 9) if tiles <= at_once[k - 2]])
+            assert ks == 1 or tiles <= held
+    held = " 148 93 71 56 45 37 33"
+    # 46 to 48 tiles: 45 clusters of six are held, so five parts; few steps, and partial sums that do not fit, split less
+    assert ask([f"split {t} 112 1 8{held}" for t in (45, 46, 48)] + [f"split 10 35 10 8{held}", f"split 10 112 1 4{held}"]) == [
+        "6 45", "5 56", "5 56", "3 93", "4 71"]
