@@ -33,36 +33,9 @@ using namespace tc;
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int W_ROWS = 128, BK = 128;
-constexpr int BAR_BYTES = 256;
-
-template <int NP, int CTAS>     // CTAS: per SM
-struct Cfg {
-  static constexpr int W_BYTES = W_ROWS * BK, X_BYTES = NP * BK;
-  static constexpr int STAGE = W_BYTES + X_BYTES;         // one 128-byte K-slice
-  // Tokens are owned, staged and sent G at a time.  Partial sums that arrive from
-  // the ks - 1 others, [source][token of the owner][row], have an area of their
-  // own up to 64 tokens; for more they share the ring with those to be sent.
-  static constexpr int G = NP <= 32 ? 4 : 16;
-  static constexpr int PART = NP <= 16 ? 14 * 1024 : NP <= 32 ? 16 * 1024 : 32 * 1024;
-  static constexpr bool OVERLAY = NP > 64 || CTAS == 1;
-  // the SM's 228 KB less 1 KB per CTA, and the barriers, the alignment and the static part
-  static constexpr int STAGES_FIT = (233472 / CTAS - 1024 - 1024 - BAR_BYTES - NP * 4 - 64 - (OVERLAY ? 0 : PART)) / STAGE;
-  static constexpr int STAGES = STAGES_FIT < 8 ? STAGES_FIT : 8;
-  static constexpr int RING = STAGES * STAGE;
-  static constexpr int SMEM = RING + (OVERLAY ? 0 : PART) + BAR_BYTES + 1024;
-  static constexpr uint32_t TMEM_COLS = NP < 32 ? 32 : NP;
-  // Of k CTAs: tokens per owner, and whether what is sent and what arrives fits.
-  static int per_owner(int M, int k) { return (M + G * k - 1) / (G * k) * G; }
-  static bool fits(int M, int k) {
-    const int t = per_owner(M, k), all = (M + G - 1) / G * G;
-    const int sent = (all - std::max(0, all - (k - 1) * t)) * 512, arrives = (k - 1) * t * 512;   // at most, by the last CTA
-    return OVERLAY ? sent + arrives <= RING : sent <= RING && arrives <= PART;
-  }
-  static_assert((2 * STAGES + 2) * 8 + 16 + 8 <= BAR_BYTES, "barrier block");
-  static_assert(SMEM <= 232448, "shared memory budget");
-  static_assert(X_BYTES % 1024 == 0 && STAGE % 1024 == 0, "128-byte swizzle atoms");
-};
+using i8::BK;
+using i8::W_ROWS;
+template <int NP, int CTAS> using Cfg = i8::FewCfg<NP, CTAS>;
 
 struct Params {
   const float* a_scales;
@@ -373,8 +346,7 @@ cudaError_t launch_out(const I8GemmArgs& g, int num_sms, cudaStream_t stream) {
 double i8_gemm_few_ns(int64_t M, int64_t N, int64_t K, int num_sms) {
   const int64_t tiles = (N + W_ROWS - 1) / W_ROWS;
   const int k_steps = (int)((K + BK - 1) / BK), ks = choose_ks<256, 1>(M, tiles, k_steps, num_sms);
-  const int64_t waves = (tiles * ks + num_sms - 1) / num_sms;
-  return 10000.0 + 460.0 * (double)waves * (double)((k_steps + ks - 1) / ks);
+  return i8::few_ns(tiles, k_steps, ks, num_sms);
 }
 
 cudaError_t launch_i8_gemm_few(const I8GemmArgs& g, int num_sms, cudaStream_t stream) {

@@ -66,6 +66,38 @@ inline int token_group(int tok_blocks, int64_t block_bytes) {
   return (int)((tok_blocks + groups - 1) / groups);
 }
 
+// k_i8_few: a row tile of W, and the barriers' block.
+constexpr int W_ROWS = 128, FEW_BAR_BYTES = 256;
+
+// k_i8_few's shared and tensor memory for NP tokens.
+template <int NP, int CTAS>     // CTAS: per SM
+struct FewCfg {
+  static constexpr int W_BYTES = W_ROWS * BK, X_BYTES = NP * BK;
+  static constexpr int STAGE = W_BYTES + X_BYTES;         // one 128-byte K-slice
+  // Tokens are owned, staged and sent G at a time.  Partial sums that arrive from
+  // the ks - 1 others, [source][token of the owner][row], have an area of their
+  // own up to 64 tokens; for more they share the ring with those to be sent.
+  static constexpr int G = NP <= 32 ? 4 : 16;
+  static constexpr int PART = NP <= 16 ? 14 * 1024 : NP <= 32 ? 16 * 1024 : 32 * 1024;
+  static constexpr bool OVERLAY = NP > 64 || CTAS == 1;
+  // the SM's 228 KB less 1 KB per CTA, and the barriers, the alignment and the static part
+  static constexpr int STAGES_FIT = (233472 / CTAS - 1024 - 1024 - FEW_BAR_BYTES - NP * 4 - 64 - (OVERLAY ? 0 : PART)) / STAGE;
+  static constexpr int STAGES = STAGES_FIT < 8 ? STAGES_FIT : 8;
+  static constexpr int RING = STAGES * STAGE;
+  static constexpr int SMEM = RING + (OVERLAY ? 0 : PART) + FEW_BAR_BYTES + 1024;
+  static constexpr uint32_t TMEM_COLS = NP < 32 ? 32 : NP;
+  // Of k CTAs: tokens per owner, and whether what is sent and what arrives fits.
+  static int per_owner(int M, int k) { return (M + G * k - 1) / (G * k) * G; }
+  static bool fits(int M, int k) {
+    const int t = per_owner(M, k), all = (M + G - 1) / G * G;
+    const int sent = (all - std::max(0, all - (k - 1) * t)) * 512, arrives = (k - 1) * t * 512;   // at most, by the last CTA
+    return OVERLAY ? sent + arrives <= RING : sent <= RING && arrives <= PART;
+  }
+  static_assert((2 * STAGES + 2) * 8 + 16 + 8 <= FEW_BAR_BYTES, "barrier block");
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(X_BYTES % 1024 == 0 && STAGE % 1024 == 0, "128-byte swizzle atoms");
+};
+
 // k_i8_few: the largest split of K, up to eight CTAs a cluster, that leaves each CTA
 // `least` steps of K to pay for joining them, whose partial sums fit (fits(k)) and
 // whose clusters, one a tile, all run at once: the device holds held(k) of them.
@@ -74,6 +106,12 @@ int split_of_k(int64_t tiles, int k_steps, int least, Fits fits, Held held) {
   for (int k = 8; k >= 2; --k)
     if (k * least <= k_steps && fits(k) && tiles <= held(k)) return k;
   return 1;
+}
+
+// Estimated time of k_i8_few for 129 to 256 tokens with K in ks parts.
+inline double few_ns(int64_t tiles, int k_steps, int ks, int num_sms) {
+  const int64_t waves = (tiles * ks + num_sms - 1) / num_sms;
+  return 10000.0 + 460.0 * (double)waves * (double)((k_steps + ks - 1) / ks);
 }
 
 // An answer of the device that does not change, asked once.

@@ -14,3 +14,12 @@ TILES = [
 ]
 # M, N, K, blocks of tokens, blocks a group: several groups, the last one short
 GROUPS = [(1280, 600, 65536, 5, 2), (2500, 3000, 29584, 10, 4), (1044, 1834, 29584, 9, 5)]
+# M, N, K, parts of K: 129 to 256 tokens that take the split-K kernel instead of tiles, every split that the rule takes
+# for them on 148 SMs
+SPLITS = [
+    (145, 5098, 7952, 3), (240, 4500, 28672, 3), (129, 37, 5936, 4), (255, 3900, 9008, 4), (256, 1900, 10000, 4),
+    (136, 32, 7024, 5), (201, 2600, 9008, 5), (129, 33, 8208, 6), (131, 36, 9872, 7), (199, 1900, 20000, 7),
+    (131, 33, 11680, 8), (160, 1500, 131056, 8),
+]
+# clusters of 2 to 8 CTAs that 148 SMs held, at one CTA per SM and at two
+HELD = {1: (74, 45, 33, 26, 22, 15, 15), 2: (148, 93, 71, 56, 45, 37, 33)}

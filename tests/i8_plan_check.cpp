@@ -4,6 +4,8 @@
 //   tiles M N K SMS                               -> bn, swap, token blocks, their group, tiles
 //   split TILES K_STEPS LEAST LARGEST HELD2 .. HELD8 -> split of K where up to LARGEST parts fit and the device holds
 //                                                    HELDk clusters of k, and the number of clusters that it holds
+//   few M N K SMS HELD2 .. HELD8                  -> for 129 to 256 tokens: whether K is split instead of tiled, and the
+//                                                    split
 //   held FIRST SECOND                             -> three answers of asked_once (guess 5) where the device gives
 //                                                    FIRST, then SECOND, and how often it was asked
 #include <cstdio>
@@ -53,6 +55,16 @@ static void split(int64_t tiles, int k_steps, int least, int largest) {
   std::printf("%d %d\n", ks, ks == 1 ? 0 : used);
 }
 
+static void few(int64_t M, int64_t N, int64_t K, int sms) {
+  int n[9];
+  for (int k = 2; k <= 8; ++k)
+    if (std::scanf("%d", &n[k]) != 1) return;
+  const int64_t row_tiles = (N + W_ROWS - 1) / W_ROWS;
+  const int k_steps = (int)((K + BK - 1) / BK);
+  const int ks = split_of_k(row_tiles, k_steps, 10, [&](int k) { return FewCfg<256, 1>::fits((int)M, k); }, [&](int k) { return n[k]; });
+  std::printf("%d %d\n", few_ns(row_tiles, k_steps, ks, sms) < choose_tiles(M, N, K, sms).ns ? 1 : 0, ks);
+}
+
 static void held(int first, int second) {
   std::atomic<int> slot{0};
   int asked = 0;
@@ -69,6 +81,7 @@ int main() {
     else if (!std::strcmp(what, "tiles") && std::scanf("%lld %lld %lld %lld", &a, &b, &c, &d) == 4) tiles(a, b, c, (int)d);
     else if (!std::strcmp(what, "held") && std::scanf("%lld %lld", &a, &b) == 2) held((int)a, (int)b);
     else if (!std::strcmp(what, "split") && std::scanf("%lld %lld %lld %lld", &a, &b, &c, &d) == 4) split(a, (int)b, (int)c, (int)d);
+    else if (!std::strcmp(what, "few") && std::scanf("%lld %lld %lld %lld", &a, &b, &c, &d) == 4) few(a, b, c, (int)d);
     else return 2;
     std::fflush(stdout);
   }

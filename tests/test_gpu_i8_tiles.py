@@ -1,12 +1,12 @@
-"""The tile kernel of the 8-bit integer linear (more tokens than the split-K kernel takes): its waits, its widths, the
-order of its tiles."""
+"""The tensor-core kernels of the 8-bit integer linear: the tile kernel's waits, widths and order of tiles, and the splits of
+K, at shapes that reach each of them."""
 import time
 
 import pytest
 import torch
 
 import nvfp4_block_scaled_18_b200 as nv
-from i8_cases import GROUPS, TILES
+from i8_cases import GROUPS, SPLITS, TILES
 
 pytestmark = pytest.mark.gpu
 BF, F32, I8 = torch.bfloat16, torch.float32, torch.int8
@@ -86,3 +86,17 @@ def test_every_width(M, N, K, bn, swap, out):
 @pytest.mark.parametrize("M,N,K,tok,group", GROUPS)
 def test_groups_of_tokens(M, N, K, tok, group):
     check(M, N, K, BF, True, 0)
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("M,N,K,ks", SPLITS)
+def test_split_of_k_for_many_tokens(M, N, K, ks, out):
+    check(M, N, K, out, N % 2 == 0, M % 3)
+
+
+@pytest.mark.parametrize("M", [13, 30, 50, 100])
+@pytest.mark.parametrize("row_tiles", [3, 20, 40, 45, 47, 60, 80, 120, 160])
+def test_split_of_k_for_few_tokens(M, row_tiles):
+    """Every split for every padding of the tokens, and row tiles that leave none."""
+    for K in (912, 3088, 9008):
+        check(M, 128 * row_tiles - 5, K, BF if K == 3088 else F32, M % 4 == 0, 0)

@@ -5,7 +5,7 @@ import subprocess
 
 import pytest
 
-from i8_cases import GROUPS, TILES
+from i8_cases import GROUPS, HELD, SPLITS, TILES
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "nvfp4_block_scaled_18_b200", "csrc")
@@ -70,13 +70,23 @@ def test_failed_query_is_asked_again(ask):
 def test_split_runs_in_one_wave(ask):
     """K is split as far as the clusters of all tiles are held at once, with the numbers of clusters of 2 to 8 that 148
     SMs held at one CTA per SM and at two."""
-    for at_once in ((74, 45, 33, 26, 22, 15, 15), (148, 93, 71, 56, 45, 37, 33)):
+    for at_once in HELD.values():
         lines = [f"split {t} 112 1 8 " + " ".join(map(str, at_once)) for t in range(1, 160)]
         for tiles, answer in enumerate(ask(lines), 1):
             ks, held = map(int, answer.split())
             assert ks == max([1] + [k for k in range(2, 9) if tiles <= at_once[k - 2]])
             assert ks == 1 or tiles <= held
-    held = " 148 93 71 56 45 37 33"
+    held = " " + " ".join(map(str, HELD[2]))
     # 46 to 48 tiles: 45 clusters of six are held, so five parts; few steps, and partial sums that do not fit, split less
     assert ask([f"split {t} 112 1 8{held}" for t in (45, 46, 48)] + [f"split 10 35 10 8{held}", f"split 10 112 1 4{held}"]) == [
         "6 45", "5 56", "5 56", "3 93", "4 71"]
+
+
+def test_cases_reach_every_split(ask):
+    """The GPU tests' shapes of 129 to 256 tokens take the split-K kernel, in the parts that they name; no other split is
+    taken over the whole range."""
+    held = " ".join(map(str, HELD[1]))
+    assert ask([f"few {m} {n} {k} 148 {held}" for m, n, k, _ in SPLITS]) == [f"1 {ks}" for *_, ks in SPLITS]
+    sizes = [(m, n, k) for m in range(129, 257, 9) for n in range(64, 28700, 613) for k in (64, 1040, 4096, 9008, 14336, 27648)]
+    taken = {a for a in ask([f"few {m} {n} {k} 148 {held}" for m, n, k in sizes]) if a[0] == "1"}
+    assert taken <= {f"1 {ks}" for *_, ks in SPLITS}
