@@ -351,8 +351,8 @@ nvfp4_status nvfp4_i8_quantize(const void* x, nvfp4_dtype dt, int64_t M, int64_t
  * mean, rstd: device, M floats each, what the backward pass reads, or NULL.
  * y may be x itself (same pointer and stride) when K <= 8192.
  * A row with a NaN or an infinity gives NaN and sets NVFP4_ERR_NONFINITE in
- * *dev_status; so does eps = 0 with a constant row.  x and K as
- * nvfp4_i8_quantize. */
+ * *dev_status; so does eps = 0 with a constant row, and a row with a difference
+ * from its mean beyond fp32 sets it too.  x and K as nvfp4_i8_quantize. */
 nvfp4_status nvfp4_layernorm(const void* x, nvfp4_dtype dt, int64_t M, int64_t K, int64_t ldx, const void* gamma,
                              const void* beta, nvfp4_dtype pdt, float eps, void* y, int64_t ldy, float* mean,
                              float* rstd, int* dev_status, void* stream);

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(ONE ? max_threads(V) : 1024) k_rows(const RowA
           }
       }
       rstd = rsqrt_rounded(team.sum(s0 + s1, red_sum[1] + base) * inv_k + (double)a.eps);
-      if (t == 0 && !(abs_key(mean) < 0x7F800000u && abs_key(rstd) < 0x7F800000u)) report_status(a.st, NVFP4_ERR_NONFINITE);
+      if (t == 0 && !has_norm(mean, rstd)) report_status(a.st, NVFP4_ERR_NONFINITE);
     }
     // the row's result before its last rounding; v holds chunk c, as x - mean
     auto finish = [&](int c) {
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kNormThreads, 1) k_norm_rows(const RowArgs a) 
     }
     const float rstd =
         rsqrt_rounded(total((s[0] + s[1]) + (s[2] + s[3]), red_sum[1] + base) * inv_k + (double)a.eps);
-    if (t == 0 && !(abs_key(mean) < 0x7F800000u && abs_key(rstd) < 0x7F800000u)) report_status(a.st, NVFP4_ERR_NONFINITE);
+    if (t == 0 && !has_norm(mean, rstd)) report_status(a.st, NVFP4_ERR_NONFINITE);
     auto result = [&](int i, float (&v)[8]) {             // before its last rounding
       const int u = i * span + t;
       float p[8];

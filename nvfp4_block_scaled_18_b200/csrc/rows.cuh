@@ -76,6 +76,12 @@ __device__ __forceinline__ float rsqrt_rounded(double x) {
   return (float)(1.0 / sqrt(x));
 }
 
+// Whether a row's statistics give it a norm: both finite, and rstd not the 0 that
+// comes of a difference from the mean beyond fp32.
+__device__ __forceinline__ bool has_norm(float mean, float rstd) {
+  return abs_key(mean) < 0x7F800000u && abs_key(rstd) - 1u < 0x7F7FFFFFu;
+}
+
 // A unit is eight elements of a row, and what one thread handles at a time: of
 // bf16 rows 16 bytes, elements 8u..8u+7; of fp32 rows two runs of 16 bytes, one
 // from each half of the row, elements 4u..4u+3 and K/2 + 4u..K/2 + 4u+3, so that

@@ -269,3 +269,20 @@ def test_layernorm_gradient_is_the_slope():
             # gradients: 64 half steps of fp32 of the summed magnitudes
             scale = float(np.abs(grad.double().cpu().numpy() * way).sum()) + float(np.abs(dy).sum())
             assert abs(slope - got) <= scale * (64 * HALF + 100 * h * h + 2.0 ** -50 / h)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows,cols", [(3, 64), (500, 16384)])
+def test_layernorm_differences_beyond_fp32(rows, cols, dtype):
+    """A finite row whose largest difference from its mean overflows fp32 has no norm, and that is reported."""
+    x = torch.randn(rows, cols, device="cuda").to(dtype)
+    x[1] = -3e38
+    x[1, 5] = 3e38
+    y, st = torch.empty_like(x), status()
+    nv.nvfp4_layernorm(x, y, dev_status=st)
+    assert st.item() == 5 and torch.isnan(y[1, 5])
+    assert torch.isfinite(y[torch.arange(rows) != 1]).all()
+    codes, scales, st = torch.empty(rows, cols, dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda"), status()
+    nv.nvfp4_layernorm_i8_quantize(x, codes, scales, dev_status=st)
+    assert st.item() == 5 and torch.isnan(scales[1]) and not codes[1].any()
+    assert torch.isfinite(scales[torch.arange(rows) != 1]).all()
