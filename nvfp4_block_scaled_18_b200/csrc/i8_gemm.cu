@@ -6,7 +6,7 @@
 // their order is free.  The epilogue rounds the sum to fp32, multiplies by the
 // token's and then the channel's scale, adds the bias and rounds to Y's type.
 //
-// Structure (persistent; CG = 2: a pair of CTAs shares one 256-row tile, each
+// Structure (persistent; a pair of CTAs shares one 256-row tile, each
 // holding 128 rows of A and of the accumulator and half of the W rows; 384
 // threads per CTA):
 //   warp 0     loads each stage by TMA (128-byte K-slices, 128-byte swizzle)
@@ -38,6 +38,7 @@ namespace nvfp4 {
 using namespace tc;
 namespace {
 
+constexpr int CG = 2;                   // CTAs of a pair
 constexpr int BM = 128;                 // rows of A per CTA
 using i8::BK;                           // bytes (= elements) of K per stage: one swizzle row
 using i8::BN_MAX;                       // columns per tile, at most
@@ -55,7 +56,7 @@ static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 static_assert((2 * MAX_STAGES + 5) * 8 + 16 + 8 <= BAR_BYTES, "barrier block");
 
 // A stage holds 128 rows of A and bn / CG rows of W; the ring takes as many as fit.
-__host__ __device__ constexpr int stage_bytes(int cg, int bn) { return A_BYTES + bn / cg * BK; }
+__host__ __device__ constexpr int stage_bytes(int bn) { return A_BYTES + bn / CG * BK; }
 
 struct Params {
   const float* a_scales;
@@ -64,7 +65,7 @@ struct Params {
   void* y;
   int64_t ldy;
   int y_align;        // bytes that Y's base and row pitch are multiples of: 16, 4 or 2
-  int M, N, K;        // of the tiles: SWAP has the channels as M and the tokens as N
+  int M, N;           // of the tiles: SWAP has the channels as M and the tokens as N
   int bn;             // columns per tile, a multiple of 32
   int stages;         // of the ring
   i8::TileOrder order;
@@ -74,30 +75,25 @@ struct Params {
   int hold;
 };
 
-// CG = 2: the copy lands in this CTA, its bytes count on the leader's barrier
-// (the same offset in the even-ranked CTA of the pair).
-template <int CG>
+// The copy lands in this CTA, its bytes count on the leader's barrier (the same
+// offset in the even-ranked CTA of the pair).
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
-  if constexpr (CG == 2)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar & 0xFEFFFFFFu)
-        : "memory");
-  else
-    tma_load_2d(dst, map, c0, c1, bar);
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar & 0xFEFFFFFFu)
+      : "memory");
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t remote_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
 }
 // A whole warp's bounded wait: the same answer for every lane.
-template <int CG>
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, WaitState* w, int* st) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait_inline<CG == 2>(bar, parity, w, st)) != 0;
+  return __all_sync(0xFFFFFFFFu, mbar_wait_inline<true>(bar, parity, w, st)) != 0;
 }
 
 // SWAP: the tiles' rows are channels (W is the tensor cores' A) and their columns
 // tokens, for token counts that fill tiles better along the columns' finer grid.
-template <int CG, bool BF16OUT, bool SWAP>
+template <bool BF16OUT, bool SWAP>
 __global__ void __launch_bounds__(THREADS, 1)
     k_i8_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -105,7 +101,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t* epi = reinterpret_cast<uint32_t*>(smem + RING_BYTES);
   float* cols = reinterpret_cast<float*>(smem + RING_BYTES + EPI_BYTES);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + RING_BYTES + EPI_BYTES + COL_BYTES);
-  uint64_t* full = bars;                      // [stages] tiles landed (CG = 2: the leader's, for both CTAs)
+  uint64_t* full = bars;                      // [stages] tiles landed (the leader's, for both CTAs)
   uint64_t* empty = bars + MAX_STAGES;        // [stages] MMAs done
   uint64_t* acc_full = bars + 2 * MAX_STAGES; // [2]
   uint64_t* acc_empty = acc_full + 2;         // [2] the epilogue has read the accumulator (the leader's counts both CTAs)
@@ -115,7 +111,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+  const uint32_t rank = cluster_ctarank();
   const int group = blockIdx.x / CG, groups = gridDim.x / CG;
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -134,21 +130,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    if constexpr (CG == 2) {
-      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)),
-                   "r"(TMEM_COLS)
-                   : "memory");
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    } else {
-      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)),
-                   "r"(TMEM_COLS)
-                   : "memory");
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   tc_fence_before();
-  if constexpr (CG == 2) cluster_sync();   // the peer's barriers exist
-  else __syncthreads();
+  cluster_sync();   // the peer's barriers exist
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
@@ -156,7 +143,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == 0) {
     // -------------------------------------------------------- TMA producer
     const uint32_t bytes = (uint32_t)(CG * A_BYTES + p.bn * BK);   // of both CTAs
-    const int stage = stage_bytes(CG, p.bn);
+    const int stage = stage_bytes(p.bn);
     int s = 0, issued = 0;
     uint32_t ph = 0;
     bool ok = p.hold != kHoldLoads;
@@ -166,13 +153,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int mb = SWAP ? ch : tok, nb = SWAP ? tok : ch;
       const int a_row = (mb * CG + (int)rank) * BM, w_row = nb * p.bn + (int)rank * (p.bn / CG);
       for (int kt = 0; kt < p.k_tiles; ++kt) {
-        ok = wait_all<CG>(saddr(&empty[s]), ph ^ 1u, ws, p.st);
+        ok = wait_all(saddr(&empty[s]), ph ^ 1u, ws, p.st);
         if (!ok) break;
         const uint32_t dst = saddr(smem) + (uint32_t)(s * stage), bar = saddr(&full[s]);
         if (elect_one()) {
           if (rank == 0) mbar_expect_tx(bar, bytes);
-          load_2d<CG>(dst, &tmA, kt * BK, a_row, bar);
-          load_2d<CG>(dst + A_BYTES, &tmB, kt * BK, w_row, bar);
+          load_2d(dst, &tmA, kt * BK, a_row, bar);
+          load_2d(dst + A_BYTES, &tmB, kt * BK, w_row, bar);
         }
         __syncwarp();
         if (kt == 0) i8::tile_blocks(p.order, tile + groups, &tok, &ch);    // the next tile's place, off the ring's critical path
@@ -187,7 +174,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // have come to the cluster's last barrier.
     if (rank == 0) {
       for (int i = max(0, issued - p.stages); i < issued; ++i)
-        (void)mbar_drain<CG == 2>(saddr(&full[i % p.stages]), (uint32_t)((i / p.stages) & 1), ws, p.st);
+        (void)mbar_drain<true>(saddr(&full[i % p.stages]), (uint32_t)((i / p.stages) & 1), ws, p.st);
     }
     if (wait_aborted(ws)) {
       const uint64_t t0 = globaltimer();
@@ -196,18 +183,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == 1 && rank == 0) {
     // ---------------------------------------------------------- MMA issuer
     const uint32_t idesc = idesc_i8(BM * CG, p.bn);
-    const int stage = stage_bytes(CG, p.bn);
+    const int stage = stage_bytes(p.bn);
     int s = 0, local = 0;
     uint32_t ph = 0;
     bool ok = true;
     for (int tile = group; ok && tile < p.num_tiles; tile += groups, ++local) {
       const int b = local & 1;
-      ok = wait_all<CG>(saddr(&acc_empty[b]), (uint32_t)((local >> 1) & 1) ^ 1u, ws, p.st);
+      ok = wait_all(saddr(&acc_empty[b]), (uint32_t)((local >> 1) & 1) ^ 1u, ws, p.st);
       if (!ok) break;
       tc_fence_after();
       const uint32_t acc = tmem + (uint32_t)(b * BN_MAX);
       for (int kt = 0; kt < p.k_tiles; ++kt) {
-        ok = wait_all<CG>(saddr(&full[s]), ph, ws, p.st);
+        ok = wait_all(saddr(&full[s]), ph, ws, p.st);
         if (!ok) break;
         tc_fence_after();
         const uint32_t base = saddr(smem) + (uint32_t)(s * stage);
@@ -226,7 +213,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // every MMA issued has completed before TMEM can be released
     if (elect_one()) commit<CG>(saddr(mma_drain));
     __syncwarp();
-    (void)mbar_drain<CG == 2>(saddr(mma_drain), 0u, ws, p.st);
+    (void)mbar_drain<true>(saddr(mma_drain), 0u, ws, p.st);
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3, half = (warp - 4) >> 2, et = threadIdx.x - 128;
@@ -259,16 +246,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         ok = false;
       }
-      ok = ok && warp_wait<CG == 2>(saddr(&acc_full[b]), (uint32_t)((local >> 1) & 1), ws, p.st);
+      ok = ok && warp_wait<true>(saddr(&acc_full[b]), (uint32_t)((local >> 1) & 1), ws, p.st);
       if (!ok) continue;
       tc_fence_after();
       auto release = [&] {                                // this warp has read its part of the accumulator
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (CG == 2) arrive_cluster(mapa_shared(saddr(&acc_empty[b]), 0));
-          else mbar_arrive(saddr(&acc_empty[b]));
-        }
+        if (lane == 0) arrive_cluster(mapa_shared(saddr(&acc_empty[b]), 0));
       };
       // the two warps of a TMEM lane quadrant take alternate runs of W columns
       const int c_end = row0 < p.M ? n_end - n0 : 0;      // uniform across the warp
@@ -363,21 +347,17 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   __syncwarp();
   tc_fence_before();
-  if constexpr (CG == 2) cluster_sync();   // the pair's MMAs and arrivals are over before either CTA leaves
-  else __syncthreads();
+  cluster_sync();   // the pair's MMAs and arrivals are over before either CTA leaves
   if (warp == 1) {
     // the leader's last commit, issued before it came here, arrives in the other CTA too
-    if (CG == 2 && rank != 0) (void)mbar_drain<true>(saddr(mma_drain), 0u, ws, p.st);
+    if (rank != 0) (void)mbar_drain<true>(saddr(mma_drain), 0u, ws, p.st);
     __syncwarp();
     tc_fence_after();
-    if constexpr (CG == 2)
-      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
-    else
-      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TMEM_COLS) : "memory");
   }
 }
 
-template <int CG, bool SWAP>
+template <bool SWAP>
 cudaError_t launch_tiles(const I8GemmArgs& g, int bn, int num_sms, cudaStream_t stream) {
   const int64_t rows = SWAP ? g.N : g.M, columns = SWAP ? g.M : g.N;
   const int64_t mb = (rows + BM * CG - 1) / (BM * CG), nb = (columns + bn - 1) / bn;
@@ -391,15 +371,15 @@ cudaError_t launch_tiles(const I8GemmArgs& g, int bn, int num_sms, cudaStream_t 
   p.y = g.y; p.ldy = g.ldy;
   const uint64_t bytes = reinterpret_cast<uintptr_t>(g.y) | ((uint64_t)g.ldy * (g.y_bf16 ? 2 : 4));
   p.y_align = bytes % 16 == 0 ? 16 : bytes % 4 == 0 ? 4 : 2;
-  p.M = (int)rows; p.N = (int)columns; p.K = (int)g.K; p.bn = bn;
-  p.stages = std::min(MAX_STAGES, RING_BYTES / stage_bytes(CG, bn));
+  p.M = (int)rows; p.N = (int)columns; p.bn = bn;
+  p.stages = std::min(MAX_STAGES, RING_BYTES / stage_bytes(bn));
   p.num_tiles = (int)(mb * nb); p.k_tiles = (int)((g.K + BK - 1) / BK);
   p.order.tok_blocks = (int)(SWAP ? nb : mb); p.order.ch_blocks = (int)(SWAP ? mb : nb);
   p.order.group = i8::token_group(p.order.tok_blocks, (int64_t)(SWAP ? bn : BM * CG) * g.K);
   p.st = g.st;
   const WaitTest wt = wait_test();
   p.wait_ns = wt.limit_ns; p.hold = wt.hold;
-  auto kern = g.y_bf16 ? k_i8_gemm<CG, true, SWAP> : k_i8_gemm<CG, false, SWAP>;
+  auto kern = g.y_bf16 ? k_i8_gemm<true, SWAP> : k_i8_gemm<false, SWAP>;
   static SmemOnce once[2];
   cudaError_t e = once[g.y_bf16 ? 1 : 0].set(kern, SMEM_BYTES);
   if (e != cudaSuccess) return e;
@@ -414,7 +394,7 @@ cudaError_t launch_tiles(const I8GemmArgs& g, int bn, int num_sms, cudaStream_t 
   at[1].id = cudaLaunchAttributeClusterDimension;
   at[1].val.clusterDim.x = CG; at[1].val.clusterDim.y = 1; at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = CG == 2 ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, SWAP ? tmW : tmA, SWAP ? tmA : tmW, p);
 }
 
@@ -447,7 +427,7 @@ cudaError_t launch_i8_gemm(const I8GemmArgs& g, int num_sms, cudaStream_t stream
   // and 11.5 us).
   const i8::Tiles t = i8::choose_tiles(g.M, g.N, g.K, num_sms);
   if (g.M <= 256 && i8_gemm_few_ns(g.M, g.N, g.K, num_sms) < t.ns) return launch_i8_gemm_few(g, num_sms, stream);
-  return t.swap ? launch_tiles<2, true>(g, t.bn, num_sms, stream) : launch_tiles<2, false>(g, t.bn, num_sms, stream);
+  return t.swap ? launch_tiles<true>(g, t.bn, num_sms, stream) : launch_tiles<false>(g, t.bn, num_sms, stream);
 }
 
 }  // namespace nvfp4

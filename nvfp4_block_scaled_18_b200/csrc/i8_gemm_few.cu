@@ -43,7 +43,7 @@ struct Params {
   const float* bias;
   void* y;
   int64_t ldy;
-  int M, N, K;
+  int M, N;
   int per_owner;      // T: tokens of an owner, a multiple of G
   int land;           // byte offset of the arriving partial sums from the ring's start
   int k_steps;        // stages of work along K: ceil(K / 128)
@@ -306,7 +306,7 @@ cudaError_t launch_np(const I8GemmArgs& g, int num_sms, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   Params p{};
   p.a_scales = g.a_scales; p.w_scales = g.w_scales; p.bias = g.bias; p.y = g.y; p.ldy = g.ldy;
-  p.M = (int)g.M; p.N = (int)g.N; p.K = (int)g.K; p.k_steps = k_steps; p.st = g.st;
+  p.M = (int)g.M; p.N = (int)g.N; p.k_steps = k_steps; p.st = g.st;
   p.per_owner = C::per_owner((int)g.M, ks);
   p.land = C::OVERLAY ? C::RING - (ks - 1) * p.per_owner * 512 : C::RING;
   const WaitTest wt = wait_test();

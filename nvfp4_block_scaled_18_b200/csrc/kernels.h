@@ -166,7 +166,7 @@ struct I8GemmArgs {
   int* st;
 };
 cudaError_t launch_i8_gemm(const I8GemmArgs& g, int num_sms, cudaStream_t stream);
-// The same for up to eight tokens on the CUDA cores, and for up to 256 on the
+// The same for up to four tokens on the CUDA cores, and for up to 256 on the
 // tensor cores with the operands swapped; cudaErrorNotSupported beyond.
 cudaError_t launch_i8_gemv(const I8GemmArgs& g, int num_sms, cudaStream_t stream);
 cudaError_t launch_i8_gemm_few(const I8GemmArgs& g, int num_sms, cudaStream_t stream);

@@ -417,10 +417,8 @@ cudaError_t run_rows(RowArgs a, int num_sms, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
-template <typename T, typename P, bool QUANT, int V, bool FULL = false>
+template <typename T, typename P, bool QUANT, int V, bool FULL>
 cudaError_t run_norm_rows(RowArgs a, int num_sms, cudaStream_t stream) {
-  if constexpr (!FULL)
-    if (a.units % (32 * V) == 0) return run_norm_rows<T, P, QUANT, V, true>(a, num_sms, stream);
   a.warps = (a.units + 32 * V - 1) / (32 * V);
   if (a.warps > kNormThreads / 32) return cudaErrorNotSupported;
   const int64_t row = (int64_t)a.units * 8 * (int64_t)sizeof(T), params = (int64_t)a.units * 64;
@@ -439,9 +437,11 @@ cudaError_t run_norm_rows(RowArgs a, int num_sms, cudaStream_t stream) {
 // Ten or five units per thread if that leaves none idle and eight does not.
 template <typename T, typename P, bool QUANT>
 cudaError_t launch_norm_rows(const RowArgs& a, int num_sms, cudaStream_t stream) {
-  if (a.units % 256 != 0 && !QUANT && a.units % 320 == 0) return run_norm_rows<T, P, QUANT, 10>(a, num_sms, stream);
-  if (a.units % 256 != 0 && a.units % 160 == 0) return run_norm_rows<T, P, QUANT, 5>(a, num_sms, stream);
-  return run_norm_rows<T, P, QUANT, 8>(a, num_sms, stream);
+  if (a.units % 256 == 0) return run_norm_rows<T, P, QUANT, 8, true>(a, num_sms, stream);
+  if constexpr (!QUANT)
+    if (a.units % 320 == 0) return run_norm_rows<T, P, QUANT, 10, true>(a, num_sms, stream);
+  if (a.units % 160 == 0) return run_norm_rows<T, P, QUANT, 5, true>(a, num_sms, stream);
+  return run_norm_rows<T, P, QUANT, 8, false>(a, num_sms, stream);
 }
 
 // Units per thread.  Many: fewer warps share a row's reductions, and a thread has
