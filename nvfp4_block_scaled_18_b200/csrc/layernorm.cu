@@ -434,13 +434,22 @@ cudaError_t run_norm_rows(RowArgs a, int num_sms, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, k_norm_rows<T, P, QUANT, V, FULL>, a);
 }
 
-// Ten or five units per thread if that leaves none idle and eight does not.
+// Ten or five units per thread if that leaves none idle and eight does not.  Where
+// none of them fills the warps, the checks of the row's end cost registers (76 bytes
+// spilled, 272 into 8 bits), and k_rows is the faster one (4096 rows of 9216 bf16: 46
+// us, 55 here, into 8 bits 52 and 74; of 13824 fp32 into 8 bits 111 and 125), except
+// for fp32 rows (11008: 101, 65 here), for bf16 rows with fp32 parameters that take
+// four warps and more (7168: 52 and 39; 5632: 30 and 34), and into 8 bits where four
+// warps a row fill the CTA (4096 rows of 7168 fp32: 67 and 58; 1500 of 6656: 28 and
+// 25.3; not so just past a wave of 592 rows: 600 of 7168 15 and 19).
 template <typename T, typename P, bool QUANT>
 cudaError_t launch_norm_rows(const RowArgs& a, int num_sms, cudaStream_t stream) {
   if (a.units % 256 == 0) return run_norm_rows<T, P, QUANT, 8, true>(a, num_sms, stream);
   if constexpr (!QUANT)
     if (a.units % 320 == 0) return run_norm_rows<T, P, QUANT, 10, true>(a, num_sms, stream);
   if (a.units % 160 == 0) return run_norm_rows<T, P, QUANT, 5, true>(a, num_sms, stream);
+  const bool four = a.units > 768 && a.units <= 1024;
+  if (QUANT ? !four : sizeof(T) == 2 && (sizeof(P) == 2 || a.units <= 768)) return cudaErrorNotSupported;
   return run_norm_rows<T, P, QUANT, 8, false>(a, num_sms, stream);
 }
 
@@ -457,7 +466,8 @@ cudaError_t launch_rows(const RowArgs& a, int num_sms, cudaStream_t stream) {
   auto fits = [&](int v) { return a.units <= max_threads(v) * v; };
   // k_norm_rows: from 16 KB a row on (4800 x 8192 bf16: 39 us, k_rows 44; into 8 bits
   // 44 and 50; 4800 x 4096 bf16: 22.8 and 19.5), and where k_rows would read fp32
-  // parameters beside bf16 rows, two lines a load (8192 x 4096: 31 and 37 us).
+  // parameters beside bf16 rows, two lines a load (8192 x 4096: 31 and 37 us), but
+  // from 4096 rows: 3000 x 4096 16.5 and 16.3, 1400 x 4096 12.7 and 9.2.
   const int64_t row_bytes = (int64_t)a.units * 8 * (int64_t)sizeof(T);
   if constexpr (NORM)
     if (a.M > 3 * (int64_t)num_sms && (row_bytes >= 16384 || (sizeof(P) > sizeof(T) && row_bytes >= 8192 && a.M >= 4096))) {

@@ -286,3 +286,10 @@ def test_layernorm_differences_beyond_fp32(rows, cols, dtype):
     nv.nvfp4_layernorm_i8_quantize(x, codes, scales, dev_status=st)
     assert st.item() == 5 and torch.isnan(scales[1]) and not codes[1].any()
     assert torch.isfinite(scales[torch.arange(rows) != 1]).all()
+
+
+@pytest.mark.parametrize("rows,cols", [(4100, 6672), (500, 9232), (4097, 5648)])
+@pytest.mark.parametrize("dtype,pdt", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)])
+def test_layernorm_ragged_rows(rows, cols, dtype, pdt):
+    """Long rows that leave lanes of their last warp idle, in every kernel that takes them."""
+    test_layernorm(rows, cols, dtype, pdt)
