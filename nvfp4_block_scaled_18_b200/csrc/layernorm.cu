@@ -12,6 +12,7 @@
 
 #include "kernels.h"
 #include "rows.cuh"
+#include "i8_plan.h"
 #include "i8_tc.cuh"
 
 namespace nvfp4 {
@@ -406,10 +407,13 @@ cudaError_t run_rows(RowArgs a, int num_sms, cudaStream_t stream) {
   const int64_t groups = (a.M + teams - 1) / teams;
   // persistent when rows fit: as many CTAs as are resident at once, by registers
   // (8192 x 4096 bf16 with 1.6 waves of them instead: 43 us, 37 so)
-  static const int regs = [&] {
+  static std::atomic<int> known;
+  const int regs = i8::asked_once(&known, 128, [&] {
     cudaFuncAttributes fa{};
-    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess && fa.numRegs > 0 ? fa.numRegs : 128;
-  }();
+    if (cudaFuncGetAttributes(&fa, kern) == cudaSuccess) return fa.numRegs;
+    (void)cudaGetLastError();
+    return 0;
+  });
   const int ctas = std::max(1, std::min(2048 / threads, 65536 / ((regs + 7) / 8 * 8 * threads)));
   const int64_t grid = std::min<int64_t>(groups, ONE ? (int64_t)num_sms * ctas : (int64_t)1 << 30);
   cudaLaunchAttribute at;
