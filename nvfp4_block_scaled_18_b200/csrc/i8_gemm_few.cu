@@ -277,7 +277,7 @@ int clusters_at_once(int ks, int num_sms) {
         cudaOccupancyMaxActiveClusters(&n, k_few_shape, &cfg) == cudaSuccess)
       return n;
     (void)cudaGetLastError();                     // the call goes on without the answer
-    return 0;
+    return -1;
   });
 }
 

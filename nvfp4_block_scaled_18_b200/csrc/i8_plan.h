@@ -114,13 +114,13 @@ inline double few_ns(int64_t tiles, int k_steps, int ks, int num_sms) {
   return 10000.0 + 460.0 * (double)waves * (double)((k_steps + ks - 1) / ks);
 }
 
-// An answer of the device that does not change, asked once.
+// An answer of the device that does not change, asked once; ask() gives -1 for none.
 template <typename Ask>
 int asked_once(std::atomic<int>* slot, int guess, Ask ask) {
   int n = slot != nullptr ? slot->load(std::memory_order_relaxed) : 0;
   if (n > 0) return n;
   n = ask();
-  if (n <= 0) return guess;             // not known: for this call alone
+  if (n < 0) return guess;              // not known: for this call alone
   if (slot != nullptr) slot->store(n, std::memory_order_relaxed);
   return n;
 }

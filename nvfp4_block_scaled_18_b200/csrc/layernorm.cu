@@ -412,7 +412,7 @@ cudaError_t run_rows(RowArgs a, int num_sms, cudaStream_t stream) {
     cudaFuncAttributes fa{};
     if (cudaFuncGetAttributes(&fa, kern) == cudaSuccess) return fa.numRegs;
     (void)cudaGetLastError();
-    return 0;
+    return -1;
   });
   const int ctas = std::max(1, std::min(2048 / threads, 65536 / ((regs + 7) / 8 * 8 * threads)));
   const int64_t grid = std::min<int64_t>(groups, ONE ? (int64_t)num_sms * ctas : (int64_t)1 << 30);

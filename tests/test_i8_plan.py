@@ -64,7 +64,8 @@ def test_widths_taken(ask):
 
 def test_failed_query_is_asked_again(ask):
     """A query that fails gives a guess for that call alone; an answer is kept."""
-    assert ask(["held 33 7", "held 0 33", "held -1 -1"]) == ["33 33 33 1", "5 33 33 2", "5 5 5 3"]
+    assert ask(["held 33 7", "held -1 33", "held -1 -1"]) == ["33 33 33 1", "5 33 33 2", "5 5 5 3"]
+    assert ask(["held 0 0"]) == ["0 0 0 3"]              # none is an answer too
 
 
 def test_split_runs_in_one_wave(ask):
