@@ -23,10 +23,10 @@
 // warps meet at a barrier once per tile, so a warp that gave up goes on to the last
 // tile's barrier without working.
 //
-// Bound: the tensor cores, 3.5 POP/s in bursts and 3.15 under the power cap (8192 x
-// 28672 x 8192: 1080 and 1223 us); for a few waves of tiles the filling and the
-// last epilogue, some 6 us, and the last wave's idle pairs (777 x 11008 x 4096:
-// 31 us, 2.2 POP/s).
+// Bound: the tensor cores, 3.6 POP/s in bursts and 2.9 to 3.15 under the power cap
+// (8192 x 28672 x 8192: 1075 and, by the device, 1223 to 1314 us); for a few waves of
+// tiles the filling and the last epilogue, some 6 us, and the last wave's idle pairs
+// (777 x 11008 x 4096: 31.5 us, 2.2 POP/s).
 #include <algorithm>
 #include <type_traits>
 

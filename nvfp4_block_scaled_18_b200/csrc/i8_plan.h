@@ -58,9 +58,9 @@ NVFP4_HD void tile_blocks(const TileOrder& o, int tile, int* tok, int* ch) {
 }
 
 // Tokens in groups of 32 MB: 8192 x 28672 x 8192, again and again under the power
-// cap, takes 1271 us so, 1423 in one group of 67 MB, which W pushes out of L2, and
-// 1293 in groups of 17 MB, for each of which W comes once from DRAM (8192 x 4096 x
-// 14336: 337, 374 and 342 us).  block_bytes: of a block of tokens.
+// cap, takes 1281 us so, 1436 in one group of 67 MB, which W pushes out of L2, and
+// 1338 in groups of 17 MB, for each of which W comes once from DRAM (8192 x 4096 x
+// 14336: 341, 371 and 350 us; all on one device).  block_bytes: of a block of tokens.
 inline int token_group(int tok_blocks, int64_t block_bytes) {
   const int64_t most = std::max<int64_t>(1, (32ll << 20) / block_bytes), groups = (tok_blocks + most - 1) / most;
   return (int)((tok_blocks + groups - 1) / groups);

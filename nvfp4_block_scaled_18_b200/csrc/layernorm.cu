@@ -545,7 +545,7 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2* slot) {
 // spent on what is on its way), reads them once for the row's sums and the
 // parameters' gradients and once more for dx.  gamma waits in shared memory too:
 // from L1, which the ring leaves too small for it, 8192 x 8192 fp32 took 227 us.
-// Bound: bytes (8192 x 8192 fp32: 129 us, 6.25 TB/s; bf16: 95 us, where half the
+// Bound: bytes (8192 x 8192 fp32: 127 us, 6.3 TB/s; bf16: 93 us, where half the
 // bytes go with as many instructions).
 constexpr int kBwdThreads = 512, kBwdSmem = 224 * 1024, kBwdMaxStages = 4;
 
@@ -833,7 +833,9 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_ln_backward_small(const Bw
   }
 }
 
-// Rows too long for that ring.
+// Rows too long for that ring (bf16 from K = 16400 on, fp32 from 11472).
+// Bound: its reads, once per column chunk with nothing loaded ahead (4096 x 14336
+// fp32: 270 us, its bytes once 108; 4096 x 16400 bf16: 352 and 62).
 // The rows' units beyond blockDim.x * V are taken in further column chunks
 // (blockIdx.y), each of which forms the row sums over the whole row again.
 template <typename T, typename P, int V>
@@ -972,8 +974,8 @@ cudaError_t run_backward_small(const BwdArgs& a, float* dgamma, float* dbeta, cu
 template <typename T, typename P>
 cudaError_t run_backward(const BwdArgs& a, int num_sms, int* parts, cudaStream_t stream) {
   const int most = std::min(num_sms, kLnMaxParts);
-  // Units per thread: four, for more rows at a time (8192 x 8192 bf16: four 88 us,
-  // two 106), but two for short rows (8192 x 1024: 19 us, four 23) and where four
+  // Units per thread: four, for more rows at a time (8192 x 8192 bf16: four 93 us,
+  // two 112), but two for short rows (8192 x 1024: 19 us, four 23) and where four
   // leave a team no room for two rows in shared memory (8192 x 8192 fp32).
   for (int v = a.units < 256 ? 2 : 4; v >= 2; v /= 2) {
     const int warps = (a.units + 32 * v - 1) / (32 * v);
