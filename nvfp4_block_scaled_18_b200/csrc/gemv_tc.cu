@@ -77,8 +77,10 @@ struct Cfg {
   // layout from the 1024-aligned base: ring | dedicated partials | barriers;
   // +1024 covers the alignment of the dynamic shared-memory base
   static constexpr int SMEM_NEED = STAGES * STAGE + PART_DED + BAR + 1024;
-  // request that keeps at most TMEM_CTAS CTAs on an SM, so tcgen05.alloc never waits on a peer
-  static constexpr int SMEM_MIN = 233472 / (TMEM_CTAS + 1) + 1024;
+  // request that keeps at most TMEM_CTAS CTAs on an SM, so tcgen05.alloc never waits on a peer;
+  // with half the tensor memory, half the shared memory, so that it never waits on another
+  // kernel's CTAs either: three of k_decode_tc's, 128 columns each, fitted beside 80 KB
+  static constexpr int SMEM_MIN = TMEM_CTAS == 2 ? 233472 / 2 - 1024 : 233472 / (TMEM_CTAS + 1) + 1024;
   static constexpr int SMEM = SMEM_NEED > SMEM_MIN ? SMEM_NEED : SMEM_MIN;
   static constexpr int CTAS_PER_SM = (233472 / (SMEM + 1024)) < TMEM_CTAS ? (233472 / (SMEM + 1024)) : TMEM_CTAS;
   static_assert(1023 + STAGES * STAGE + PART_DED + BAR <= SMEM, "layout exceeds the shared-memory request");
@@ -88,6 +90,8 @@ struct Cfg {
   static_assert(PART_OWN || PART <= STAGES * STAGE, "partials overlay the stage ring");
   static_assert(233472 / (SMEM + 1024) <= TMEM_CTAS, "TMEM must fit every co-resident CTA");
   static_assert(CTAS_PER_SM >= 1, "residency");
+  static_assert(TMEM_CTAS == 1 || (int64_t)(SMEM + 1024) * 512 >= (int64_t)233472 * TMEM_COLS,
+                "a share of the SM's shared memory as large as that of its tensor memory");
 };
 
 struct SwapParams {

@@ -95,6 +95,8 @@ struct FewCfg {
   }
   static_assert((2 * STAGES + 2) * 8 + 16 + 8 <= FEW_BAR_BYTES, "barrier block");
   static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert((int64_t)(SMEM + 1024) * 512 >= (int64_t)233472 * TMEM_COLS,
+                "a share of the SM's shared memory as large as that of its tensor memory, so that tcgen05.alloc waits for none");
   static_assert(X_BYTES % 1024 == 0 && STAGE % 1024 == 0, "128-byte swizzle atoms");
 };
 
